@@ -12,6 +12,10 @@ Stage 1, ``avq_quantize``: full-tree key quantisation and aggregation
 ("AVQ-Attention: Adaptive Vector-Quantized Attention", Sec. 4.2, Algorithm 1).
 Stage 2, ``avq_attention``: count-weighted attention over the parents with
 top-P child refinement per query block (Sec. 4.3, Algorithm 2).
+
+Beside them, exact operators of the same layers, each with its gradient:
+``avq_rotary`` and ``avq_qk_norm`` (queries and keys before they are
+quantised) and ``avq_cross_attention`` (over another sequence).
 """
 from __future__ import annotations
 
@@ -29,6 +33,9 @@ AVQ_ERR_DEVICE, AVQ_ERR_TIMEOUT, AVQ_ERR_WORKSPACE = 4, 5, 6
 AVQ_F32, AVQ_BF16 = 0, 1
 AVQ_PATH_AUTO, AVQ_PATH_SIMT, AVQ_PATH_TC = 0, 1, 2
 AVQ_DENOM_AUTO, AVQ_DENOM_TWO_PASS, AVQ_DENOM_EXTRAPOLATED = 0, 1, 2
+AVQ_NORM_NONE, AVQ_NORM_RMS, AVQ_NORM_LAYER = 0, 1, 2
+AVQ_ROTARY_HALF, AVQ_ROTARY_INTERLEAVED = 0, 1
+AVQ_ROTARY_PLAIN, AVQ_ROTARY_LINEAR, AVQ_ROTARY_NTK, AVQ_ROTARY_YARN = 0, 1, 2, 3
 
 
 class AVQError(RuntimeError):
@@ -40,6 +47,20 @@ class AVQError(RuntimeError):
 class avq_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int),
                 ("d", ctypes.c_int), ("M0", ctypes.c_int), ("C", ctypes.c_int)]
+
+
+class avq_strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class avq_qk_dims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "N", "Hq", "Hk", "d", "rot", "axes", "pos_batch", "layout",
+                                             "norm")]
+                + [("eps", ctypes.c_float), ("mscale", ctypes.c_float)])
+
+
+class avq_cross_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Bk", "Hq", "Hk", "Nq", "Nk", "d")] + [("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -76,6 +97,23 @@ def lib() -> ctypes.CDLL:
                                           ctypes.c_int, _vp]
                 L.avq_hilbert_order.argtypes = [ctypes.c_int, _vp]
                 L.avq_gilbert_order.argtypes = [ctypes.c_int, ctypes.c_int, _vp]
+                st = P(avq_strides)
+                L.avq_rotary.argtypes = [P(avq_qk_dims), ctypes.c_int, _vp, st, _vp, st, _vp, _vp, ctypes.c_int,
+                                         _vp, _vp, _vp]
+                L.avq_qk_norm.argtypes = [P(avq_qk_dims), ctypes.c_int, _vp, st, _vp, st] + [_vp] * 9
+                L.avq_qk_norm_backward.argtypes = ([P(avq_qk_dims), ctypes.c_int] + [_vp, st] * 4 + [_vp] * 10
+                                                   + [_vp, ctypes.c_size_t, _vp])
+                L.avq_qk_norm_workspace_size.argtypes = [P(avq_qk_dims), ctypes.c_int]
+                L.avq_qk_norm_workspace_size.restype = ctypes.c_size_t
+                L.avq_rotary_freqs.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_double, ctypes.c_int,
+                                               ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
+                                               _vp, _vp]
+                L.avq_cross_attention.argtypes = ([P(avq_cross_dims), ctypes.c_int] + [_vp, st] * 3
+                                                  + [_vp, _vp, _vp, st, _vp, _vp, ctypes.c_size_t, _vp])
+                L.avq_cross_attention_backward.argtypes = ([P(avq_cross_dims), ctypes.c_int] + [_vp, st] * 5
+                                                           + [_vp] * 7 + [ctypes.c_size_t, _vp])
+                L.avq_cross_workspace_size.argtypes = [P(avq_cross_dims), ctypes.c_int, ctypes.c_int]
+                L.avq_cross_workspace_size.restype = ctypes.c_size_t
                 L.avq_selftest_wait.argtypes = [ctypes.c_int, _vp]
                 L.avq_selftest_exp2.argtypes = [_vp, _vp, ctypes.c_int64, _vp]
                 L.avq_workspace_size.argtypes = [P(avq_dims), ctypes.c_int, ctypes.c_int,
@@ -91,7 +129,9 @@ def lib() -> ctypes.CDLL:
                 for name in ("avq_quantize", "avq_quantize_noalloc", "avq_attention", "avq_permute",
                              "avq_quantize3", "avq_attention3",
                              "avq_hilbert_order", "avq_gilbert_order", "avq_check_device",
-                             "avq_codebook_update", "avq_selftest_wait", "avq_selftest_exp2"):
+                             "avq_codebook_update", "avq_selftest_wait", "avq_selftest_exp2",
+                             "avq_rotary", "avq_qk_norm", "avq_qk_norm_backward", "avq_rotary_freqs",
+                             "avq_cross_attention", "avq_cross_attention_backward"):
                     getattr(L, name).restype = ctypes.c_int
                 _lib = L
     return _lib
@@ -439,6 +479,261 @@ def avq_gilbert_order(width: int, height: int) -> torch.Tensor:
     out = torch.empty(max(1, int(width) * int(height)), dtype=torch.int32)  # sizes checked by the library
     _check(lib().avq_gilbert_order(int(width), int(height), _vp(out.data_ptr())))
     return out
+
+
+def _view(t, name, shape=None, dtype=None, device=None):
+    """Pointer and strides of a [B,H,N,d] CUDA tensor whose last dimension is
+    contiguous (any view of that kind: heads inside a joint projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, H, N, d], got {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device} (all tensors on one GPU)")
+    if t.stride(3) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return _vp(t.data_ptr()), avq_strides(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _no_view(t):
+    return None, avq_strides(0, 0, 0)
+
+
+def _launch(dev, stream):
+    """Context in which a call allocates and launches: `dev` current and, when the
+    caller names a stream, that stream current too, so that outputs and
+    workspaces made here come from (and go back to) that stream's memory."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, expected {dev}")
+    return torch.cuda.stream(stream)
+
+
+_NORMS = {"rms": AVQ_NORM_RMS, "layer": AVQ_NORM_LAYER}
+_LAYOUTS = {"half": AVQ_ROTARY_HALF, "interleaved": AVQ_ROTARY_INTERLEAVED}
+_SCALINGS = {"none": AVQ_ROTARY_PLAIN, "linear": AVQ_ROTARY_LINEAR, "ntk": AVQ_ROTARY_NTK, "yarn": AVQ_ROTARY_YARN}
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _qk_dims(Q, K, norm, eps, freqs, positions, layout, mscale, axes):
+    """Dims, position and frequency tensors of a norm or rotation call, checked."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
+        raise ValueError("Q must be a [B, H, N, d] tensor")
+    B, Hq, N, d = Q.shape
+    Hk = 0
+    if K is not None:
+        if not isinstance(K, torch.Tensor) or K.dim() != 4 or (K.shape[0], K.shape[2], K.shape[3]) != (B, N, d):
+            raise ValueError("K must be [B, Hk, N, d] like Q")
+        Hk = K.shape[1]
+    rot, pos_batch = 0, 0
+    if freqs is not None:
+        rot = 2 * freqs.numel()
+        _expect(freqs, "freqs", (freqs.numel(),), torch.float64, Q.device)
+        if positions is not None:
+            tail = (2,) if axes == 2 else ()
+            pos_batch = int(positions.dim() == 2 + len(tail))
+            _expect(positions, "positions", ((B, N) if pos_batch else (N,)) + tail, torch.int32, Q.device)
+    elif positions is not None:
+        raise ValueError("positions need freqs")
+    dims = avq_qk_dims(B, N, Hq, Hk, d, rot, int(axes), pos_batch, _choice(_LAYOUTS, layout, "layout"), norm,
+                       float(eps), float(mscale))
+    return dims, (positions if freqs is not None else None)
+
+
+def _qk_outputs(Q, K, Yq, Yk):
+    _expect(Yq, "the queries' output", Q.shape, Q.dtype, Q.device)
+    if Yq is None:
+        Yq = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    if K is None:
+        return Yq, None
+    _expect(Yk, "the keys' output", K.shape, Q.dtype, Q.device)
+    if Yk is None:
+        Yk = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
+    return Yq, Yk
+
+
+def avq_rotary_freqs(rot: int, base: float = 10000.0, axes: int = 1, scaling: str = "none", factor: float = 1.0,
+                     trained: int = 4096, turns_low: float = 1.0, turns_high: float = 32.0, device="cpu"):
+    """Frequencies of a rotation of `rot` elements (float64 [rot/2], on `device`)
+    and the factor on sine and cosine.  scaling: "none", "linear", "ntk" or
+    "yarn", stretching positions by `factor` beyond the `trained` range."""
+    out = torch.empty(max(1, int(rot) // 2), dtype=torch.float64)
+    m = ctypes.c_float(1.0)
+    _check(lib().avq_rotary_freqs(int(rot), int(axes), float(base), _choice(_SCALINGS, scaling, "scaling"),
+                                  float(factor), int(trained), float(turns_low), float(turns_high),
+                                  _vp(out.data_ptr()), ctypes.byref(m)))
+    return out.to(device), m.value
+
+
+def avq_rotary(Q, K=None, freqs=None, positions=None, layout="half", mscale=1.0, axes=1, inverse=False, Yq=None,
+               Yk=None, stream=None):
+    """Rotation by position of Q [B,Hq,N,d] and K [B,Hk,N,d] (or None), views
+    with a contiguous last dimension.  freqs float64 [rot/2] on the GPU: the
+    leading `rot` elements of each head turn; positions int32 [N] or [B,N],
+    with axes=2 [N,2] or [B,N,2] (None: 0..N-1); layout "half" or
+    "interleaved".  Returns dense (Yq, Yk).  `inverse` turns the other way:
+    the gradient of the forward call."""
+    if freqs is None:
+        raise ValueError("freqs is needed")
+    dims, positions = _qk_dims(Q, K, AVQ_NORM_NONE, 0.0, freqs, positions, layout, mscale, axes)
+    dt, dev = _dtype_code(Q), Q.device
+    qp, qs = _view(Q, "Q")
+    kp, ks = _no_view(K) if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    with _launch(dev, stream):
+        Yq, Yk = _qk_outputs(Q, K, Yq, Yk)
+        _check(lib().avq_rotary(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks),
+                                _ptr(positions), _ptr(freqs), int(bool(inverse)), _ptr(Yq), _ptr(Yk),
+                                _stream(None)))
+    return Yq, Yk
+
+
+def avq_qk_norm(Q, K=None, q_weight=None, k_weight=None, q_bias=None, k_bias=None, norm="rms", eps=1e-6, freqs=None,
+                positions=None, layout="half", mscale=1.0, axes=1, Yq=None, Yk=None, stream=None):
+    """RMS or LayerNorm (norm "rms" or "layer") of every head of Q [B,Hq,N,d] and
+    K [B,Hk,N,d] (or None), then, with freqs, the rotation of avq_rotary, in
+    one pass.  Weights and biases [d] in Q's dtype, or None.  Returns dense
+    (Yq, Yk)."""
+    dims, positions = _qk_dims(Q, K, _choice(_NORMS, norm, "norm"), eps, freqs, positions, layout, mscale, axes)
+    dt, dev = _dtype_code(Q), Q.device
+    qp, qs = _view(Q, "Q")
+    kp, ks = _no_view(K) if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (q_bias, "q_bias"), (k_bias, "k_bias")):
+        _expect(t, n, (dims.d,), Q.dtype, dev)
+    with _launch(dev, stream):
+        Yq, Yk = _qk_outputs(Q, K, Yq, Yk)
+        _check(lib().avq_qk_norm(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks), _ptr(q_weight),
+                                 _ptr(k_weight), _ptr(q_bias), _ptr(k_bias), _ptr(positions), _ptr(freqs), _ptr(Yq),
+                                 _ptr(Yk), _stream(None)))
+    return Yq, Yk
+
+
+def avq_qk_norm_backward(dYq, dYk, Q, K=None, q_weight=None, k_weight=None, norm="rms", eps=1e-6, bias=False,
+                         freqs=None, positions=None, layout="half", mscale=1.0, axes=1, dQ=None, dK=None, ws=None,
+                         stream=None):
+    """Gradients of avq_qk_norm.  Returns (dQ, dK, dq_weight, dk_weight, dq_bias,
+    dk_bias): dQ, dK dense in Q's dtype, the others float32 [d] (the weights'
+    where a weight was given, the biases' with bias=True, else None)."""
+    dims, positions = _qk_dims(Q, K, _choice(_NORMS, norm, "norm"), eps, freqs, positions, layout, mscale, axes)
+    if (dYk is None) != (K is None):
+        raise ValueError("dYk and K go together")
+    dt, dev = _dtype_code(Q), Q.device
+    gqp, gqs = _view(dYq, "dYq", Q.shape, Q.dtype, dev)
+    gkp, gks = _no_view(K) if K is None else _view(dYk, "dYk", K.shape, Q.dtype, dev)
+    qp, qs = _view(Q, "Q")
+    kp, ks = _no_view(K) if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _expect(t, n, (dims.d,), Q.dtype, dev)
+    wanted = (q_weight is not None, K is not None and k_weight is not None, bias, bias and K is not None)
+    with _launch(dev, stream):
+        dQ, dK = _qk_outputs(Q, K, dQ, dK)
+        sums = torch.empty((4, dims.d), dtype=torch.float32, device=dev)
+        dwq, dwk, dbq, dbk = (sums[i] if w else None for i, w in enumerate(wanted))
+        if ws is None:
+            n = int(lib().avq_qk_norm_workspace_size(ctypes.byref(dims), dt))
+            ws = torch.empty(n + 256, dtype=torch.uint8, device=dev)
+        wp, wn = _ws_ptr(ws, dev)
+        _check(lib().avq_qk_norm_backward(ctypes.byref(dims), dt, gqp, ctypes.byref(gqs), gkp, ctypes.byref(gks), qp,
+                                          ctypes.byref(qs), kp, ctypes.byref(ks), _ptr(q_weight), _ptr(k_weight),
+                                          _ptr(positions), _ptr(freqs), _ptr(dQ), _ptr(dK), _ptr(dwq), _ptr(dwk),
+                                          _ptr(dbq), _ptr(dbk), wp, wn, _stream(None)))
+    return dQ, dK, dwq, dwk, dbq, dbk
+
+
+def _cross_dims(Q, K, V, kv_lens, key_mask, scale):
+    """Dims of a cross attention call and its inputs' pointers and strides."""
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
+        raise ValueError("Q must be a [B, Hq, Nq, d] tensor")
+    B, Hq, Nq, d = Q.shape
+    dev = Q.device
+    views = [_view(Q, "Q"), _view(K, "K", None, Q.dtype, dev), _view(V, "V", K.shape, Q.dtype, dev)]
+    Bk, Hk, Nk, dk = K.shape
+    if dk != d:
+        raise ValueError(f"K must be [Bk, Hk, Nk, {d}], got {tuple(K.shape)}")
+    if Bk < 1 or Hk < 1 or B % Bk or Hq % Hk:
+        raise ValueError(f"Q's batch and heads ({B}, {Hq}) must be multiples of K's ({Bk}, {Hk})")
+    _expect(kv_lens, "kv_lens", (Bk,), torch.int32, dev)
+    if key_mask is not None:
+        if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("key_mask must be a bool or uint8 tensor")
+        _expect(key_mask, "key_mask", (Bk, Nk), None, dev)
+    scale = d ** -0.5 if scale is None else float(scale)
+    return avq_cross_dims(B, Bk, Hq, Hk, Nq, Nk, d, scale), views
+
+
+def avq_cross_workspace_size(dims: avq_cross_dims, dtype: int, backward=False) -> int:
+    return int(lib().avq_cross_workspace_size(ctypes.byref(dims), int(dtype), int(bool(backward))))
+
+
+def _cross_ws(dims, dt, backward, ws, dev):
+    if ws is None:
+        n = avq_cross_workspace_size(dims, dt, backward)
+        ws = torch.empty(n + 256, dtype=torch.uint8, device=dev) if n else None
+    return ws, *_ws_ptr(ws, dev)
+
+
+def avq_cross_attention(Q, K, V, kv_lens=None, key_mask=None, scale=None, O=None, lse=False, ws=None, stream=None):
+    """Exact attention of Q [B,Hq,Nq,d] over another sequence's K, V
+    [Bk,Hk,Nk,d] (views with a contiguous last dimension; B a multiple of Bk,
+    Hq of Hk).  kv_lens int32 [Bk]: keys from there on are left out; key_mask
+    bool [Bk,Nk]: keys where it is False are left out.  Rows with no key give
+    0.  Returns (O [B,Hq,Nq,d], lse float32 [B,Hq,Nq] or None); `O` may be a
+    view; `lse=True` asks for the log-sum-exp that the backward call needs, a
+    tensor is written in place."""
+    dims, ((qp, qs), (kp, ks), (vp, vs)) = _cross_dims(Q, K, V, kv_lens, key_mask, scale)
+    dt, dev = _dtype_code(Q), Q.device
+    with _launch(dev, stream):
+        if O is None:
+            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        op, os_ = _view(O, "O", Q.shape, Q.dtype, dev)
+        if isinstance(lse, torch.Tensor):
+            _expect(lse, "lse", Q.shape[:3], torch.float32, dev)
+        else:
+            lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=dev) if lse else None
+        ws, wp, wn = _cross_ws(dims, dt, False, ws, dev)
+        _check(lib().avq_cross_attention(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks), vp,
+                                         ctypes.byref(vs), _ptr(kv_lens), _ptr(key_mask), op, ctypes.byref(os_),
+                                         _ptr(lse), wp, wn, _stream(None)))
+    return O, lse
+
+
+def avq_cross_attention_backward(dO, Q, K, V, O, lse, kv_lens=None, key_mask=None, scale=None, dQ=None, dK=None,
+                                 dV=None, ws=None, stream=None):
+    """Gradients of avq_cross_attention from its inputs, its outputs O and lse and
+    the gradient dO of O.  Returns dense (dQ [B,Hq,Nq,d], dK, dV [Bk,Hk,Nk,d]),
+    dK and dV summed over the heads and batch entries that share them."""
+    dims, ((qp, qs), (kp, ks), (vp, vs)) = _cross_dims(Q, K, V, kv_lens, key_mask, scale)
+    dt, dev = _dtype_code(Q), Q.device
+    gp, gs = _view(dO, "dO", Q.shape, Q.dtype, dev)
+    op, os_ = _view(O, "O", Q.shape, Q.dtype, dev)
+    if lse is None:
+        raise ValueError("lse is needed: call the forward pass with lse=True")
+    _expect(lse, "lse", Q.shape[:3], torch.float32, dev)
+    for t, name, like in ((dQ, "dQ", Q), (dK, "dK", K), (dV, "dV", K)):
+        _expect(t, name, like.shape, Q.dtype, dev)
+    with _launch(dev, stream):
+        dQ, dK, dV = (torch.empty(like.shape, dtype=Q.dtype, device=dev) if t is None else t
+                      for t, like in ((dQ, Q), (dK, K), (dV, K)))
+        ws, wp, wn = _cross_ws(dims, dt, True, ws, dev)
+        _check(lib().avq_cross_attention_backward(
+            ctypes.byref(dims), dt, gp, ctypes.byref(gs), qp, ctypes.byref(qs), kp, ctypes.byref(ks), vp,
+            ctypes.byref(vs), op, ctypes.byref(os_), _ptr(lse), _ptr(kv_lens), _ptr(key_mask), _ptr(dQ), _ptr(dK),
+            _ptr(dV), wp, wn, _stream(None)))
+    return dQ, dK, dV
 
 
 def avq_selftest_wait(timeout_us: int = 2000, stream=None):

@@ -33,7 +33,7 @@ avq_status fail(avq_status s, const char* fmt, ...) {
 
 // Host-side fault injection for tests of the callers' error handling: when
 // the environment variable AVQ_FAULT names an entry point ("quantize",
-// "attention", "codebook_update", "permute") or is "all", that call returns
+// "attention", "codebook_update", "permute", ...) or is "all", that call returns
 // AVQ_ERR_CUDA after its argument checks and before anything reaches the GPU.
 bool injected(const char* entry) {
   const char* v = getenv("AVQ_FAULT");
@@ -104,6 +104,25 @@ void LaunchLog::add(const char* name) {
   len += n;
   text[len] = 0;
 }
+
+avq_status api_begin() {
+  t_error[0] = 0;
+  return AVQ_OK;
+}
+avq_status api_fail(avq_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(t_error, sizeof(t_error), fmt, ap);
+  va_end(ap);
+  return s;
+}
+avq_status api_finish(cudaError_t e, const char* where, const LaunchLog& log) {
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  snprintf(t_kernels, sizeof(t_kernels), "%s", log.text);
+  return AVQ_OK;
+}
+int api_path() { return t_path; }
+bool api_injected(const char* entry) { return injected(entry); }
 
 unsigned int* error_word() {
   const int dev = current_device();

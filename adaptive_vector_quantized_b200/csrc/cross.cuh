@@ -1,0 +1,36 @@
+// Exact attention over another sequence's keys and values: what the kernels
+// of the forward pass, the gradients and the joins share.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc_util.cuh"
+
+namespace avq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Keys of encoder sequence kb that are looked at: lengths outside [0, Nk] are
+// taken as the nearer end.
+__device__ __forceinline__ int key_count(const CrossArgs& a, int kb) {
+  if (a.kv_lens == nullptr) return a.Nk;
+  const int n = __ldg(a.kv_lens + kb);
+  return n < 0 ? 0 : (n > a.Nk ? a.Nk : n);
+}
+__device__ __forceinline__ bool key_seen(const CrossArgs& a, int kb, int j, int count) {
+  return j < count && (a.key_mask == nullptr || __ldg(a.key_mask + (size_t)kb * a.Nk + j) != 0);
+}
+
+template <typename T>
+__device__ __forceinline__ void put4(T* p, const float* v);
+template <>
+__device__ __forceinline__ void put4<float>(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <>
+__device__ __forceinline__ void put4<bf16>(bf16* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+}  // namespace avq

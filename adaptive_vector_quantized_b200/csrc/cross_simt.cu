@@ -1,0 +1,433 @@
+// Exact attention over another sequence's keys and values, and its gradients,
+// on the CUDA cores: both element types, every supported shape, and the path
+// of 32-bit inputs (tensor-core products would round them to 11 bits).
+//
+//   S = scale Q K^T over the keys that are looked at, P = softmax(S), O = P V,
+//   lse = log sum exp(S);
+//   with delta = rowsum(dO O):  dS = scale P (dO V^T - delta),
+//   dQ = dS K,  dK = dS^T Q,  dV = P^T dO  (dK, dV over every query head and
+//   sequence that shares the key head).
+// A row with no key gives O = 0, lse = -inf and dQ = 0.
+//
+// Tiles of 64 rows x 64 keys in shared memory as fp32; 256 threads, each 4 x 4
+// scores, in fma.f32x2 (two products an instruction).  All five products read
+// the tiles as they were loaded: rows against rows (S, dO V^T), rows against
+// columns (P V, dS K) and columns against columns (P^T dO, dS^T Q).  Bound by
+// the FMA pipe and, nearly, by shared memory reads (8 16-byte reads for 64
+// products).  Keys that are left out are loaded as zeros, so that infinities
+// and NaN there meet no product.
+#include "cross.cuh"
+#include "fastmath.cuh"
+
+namespace avq {
+
+namespace {
+
+constexpr int kT = 64;  // rows and keys of a tile
+constexpr int kThreads = 256;
+constexpr int kPS = kT + 4;  // row pitch of the score tiles
+
+template <int D>
+constexpr int pitch() { return D + 4; }
+
+// rows [first, first + 64) of a [.., n, d] tensor; rows outside [0, n) or not wanted are zeros
+template <typename T, int D, typename F>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride, int first, F&& want) {
+  for (int e = threadIdx.x; e < kT * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (want(r)) loadE<4>(src + (int64_t)(first + r) * row_stride + c, v);
+    *reinterpret_cast<float4*>(dst + r * pitch<D>() + c) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// acc[i][j] = sum_k A[ty + 16 i][k] B[tx + 16 j][k]
+template <int D>
+__device__ __forceinline__ void rows_rows(const float* A, const float* B, int ty, int tx, float acc[4][4]) {
+  float2 s[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = fm::f2(0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < D; k += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * pitch<D>() + k);
+      b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * pitch<D>() + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fm::fma2(fm::f2(a[i].x, a[i].y), fm::f2(b[j].x, b[j].y), s[i][j]);
+        s[i][j] = fm::fma2(fm::f2(a[i].z, a[i].w), fm::f2(b[j].z, b[j].w), s[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
+}
+
+// acc[i][c] += sum_k A[ty + 16 i][k] B[k][4 tx + 64 c ..]  (A: score tile)
+template <int D>
+__device__ __forceinline__ void rows_cols(const float* A, const float* B, int ty, int tx, float2 acc[4][D / 32]) {
+#pragma unroll 2
+  for (int k = 0; k < kT; k += 4) {
+    float4 a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPS + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(B + (k + kk) * pitch<D>() + 4 * tx + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
+          acc[i][2 * c] = fm::fma2(fm::f2(x, x), fm::f2(v.x, v.y), acc[i][2 * c]);
+          acc[i][2 * c + 1] = fm::fma2(fm::f2(x, x), fm::f2(v.z, v.w), acc[i][2 * c + 1]);
+        }
+      }
+    }
+  }
+}
+
+// acc[i][c] += sum_k A[k][4 ty + i] B[k][4 tx + 64 c ..]  (A: score tile)
+template <int D>
+__device__ __forceinline__ void cols_cols(const float* A, const float* B, int ty, int tx, float2 acc[4][D / 32]) {
+#pragma unroll 4
+  for (int k = 0; k < kT; ++k) {
+    const float4 a = *reinterpret_cast<const float4*>(A + k * kPS + 4 * ty);
+    const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const float4 v = *reinterpret_cast<const float4*>(B + k * pitch<D>() + 4 * tx + 64 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i][2 * c] = fm::fma2(fm::f2(av[i], av[i]), fm::f2(v.x, v.y), acc[i][2 * c]);
+        acc[i][2 * c + 1] = fm::fma2(fm::f2(av[i], av[i]), fm::f2(v.z, v.w), acc[i][2 * c + 1]);
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void clear(float2 acc[4][D / 32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[i][c] = fm::f2(0.f, 0.f);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cross_simt_kernel(const CrossArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float* sQ = sm;
+  float* sK = sQ + kT * pitch<D>();
+  float* sV = sK + kT * pitch<D>();
+  float* sP = sV + kT * pitch<D>();
+  __shared__ unsigned char seen[kT];
+  const int tiles = (a.Nq + kT - 1) / kT;
+  const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
+  const int b = bh / a.Hq, h = bh % a.Hq;
+  const int kb = b / (a.B / a.Bk), kh = h / (a.Hq / a.Hk);
+  const int count = key_count(a, kb);
+  const int ktiles = (count + kT - 1) / kT;
+  const int t0 = (int)((long long)ktiles * split / a.splits), t1 = (int)((long long)ktiles * (split + 1) / a.splits);
+  const int row0 = rt * kT;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const T* Q = static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h;
+  const T* K = static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h;
+  const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
+  load_tile<T, D>(sQ, Q, a.qs.n, row0, [&](int r) { return row0 + r < a.Nq; });
+  const float c2 = a.scale * kLog2e;
+  float m[4], z[4];
+  float2 o[4][D / 32];
+  clear<D>(o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, z[i] = 0.f;
+  for (int t = t0; t < t1; ++t) {
+    const int k0 = t * kT;
+    __syncthreads();  // the tiles below are still read by the last trip
+    if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
+    __syncthreads();
+    load_tile<T, D>(sK, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
+    load_tile<T, D>(sV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
+    __syncthreads();
+    float s[4][4];
+    rows_rows<D>(sQ, sK, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!seen[tx + 16 * j]) s[i][j] = -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float mn = fmaxf(m[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn * c2;
+      const float keep = m[i] == -INFINITY ? 0.f : exp2f(m[i] * c2 - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = exp2f(fmaf(s[i][j], c2, -base));
+        sum += s[i][j];
+        sP[(ty + 16 * i) * kPS + tx + 16 * j] = s[i][j];
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      z[i] = z[i] * keep + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) o[i][c] = fm::mul2(o[i][c], fm::f2(keep, keep));
+    }
+    __syncthreads();
+    rows_cols<D>(sP, sV, ty, tx, o);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + ty + 16 * i;
+    if (r >= a.Nq) continue;
+    const float inv = z[i] > 0.f ? 1.f / z[i] : (z[i] == 0.f ? 0.f : z[i]);  // NaN stays NaN
+    const float lse = z[i] == 0.f ? -INFINITY : a.scale * m[i] + logf(z[i]);
+    const size_t row = ((size_t)b * a.Hq + h) * a.Nq + r;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const float v[4] = {o[i][2 * c].x * inv, o[i][2 * c].y * inv, o[i][2 * c + 1].x * inv, o[i][2 * c + 1].y * inv};
+      if (a.splits > 1)
+        put4(a.part + ((size_t)split * a.B * a.Hq * a.Nq + row) * D + 4 * tx + 64 * c, v);
+      else
+        put4(static_cast<T*>(a.O) + b * a.os.b + h * a.os.h + r * a.os.n + 4 * tx + 64 * c, v);
+    }
+    if (tx == 0) {
+      if (a.splits > 1)
+        a.part_lse[(size_t)split * a.B * a.Hq * a.Nq + row] = lse;
+      else if (a.lse != nullptr)
+        a.lse[row] = lse;
+    }
+  }
+}
+
+// P and dS of one tile pair: rows ty + 16 i of the row tile, keys tx + 16 j.
+template <int D>
+__device__ __forceinline__ void scores_back(const float* sQ, const float* sG, const float* sK, const float* sV,
+                                            const float* sL, const float* sDelta, const unsigned char* seen, int ty,
+                                            int tx, float c2, float scale, float p[4][4], float ds[4][4]) {
+  rows_rows<D>(sQ, sK, ty, tx, p);
+  rows_rows<D>(sG, sV, ty, tx, ds);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float l = sL[ty + 16 * i], dl = sDelta[ty + 16 * i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool on = seen[tx + 16 * j] != 0 && l != -INFINITY;
+      p[i][j] = on ? exp2f(fmaf(p[i][j], c2, -l)) : 0.f;
+      ds[i][j] = on ? p[i][j] * (ds[i][j] - dl) * scale : 0.f;
+    }
+  }
+}
+
+// log-sum-exp (in base 2) and delta of a row tile; rows past the end get +inf (P = 0)
+__device__ __forceinline__ void load_rows(const CrossArgs& a, float* sL, float* sDelta, size_t head_row, int row0) {
+  if (threadIdx.x < kT) {
+    const int r = row0 + threadIdx.x;
+    sL[threadIdx.x] = r < a.Nq ? a.lse[head_row + r] * kLog2e : INFINITY;
+    sDelta[threadIdx.x] = r < a.Nq ? a.delta[head_row + r] : 0.f;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float* sK = sm;
+  float* sV = sK + kT * pitch<D>();
+  float* sQ = sV + kT * pitch<D>();
+  float* sG = sQ + kT * pitch<D>();
+  float* sP = sG + kT * pitch<D>();
+  float* sD = sP + kT * kPS;
+  __shared__ float sL[kT], sDelta[kT];
+  __shared__ unsigned char seen[kT];
+  const int tiles = (a.Nk + kT - 1) / kT;
+  const int kt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
+  const int kb = bh / a.Hk, kh = bh % a.Hk;
+  const int R = a.B / a.Bk, G = a.Hq / a.Hk;
+  const int k0 = kt * kT;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int count = key_count(a, kb);
+  if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
+  __syncthreads();
+  load_tile<T, D>(sK, static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h, a.ks.n, k0,
+                  [&](int r) { return seen[r] != 0; });
+  load_tile<T, D>(sV, static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h, a.vs.n, k0,
+                  [&](int r) { return seen[r] != 0; });
+  const float c2 = a.scale * kLog2e;
+  float2 dk[4][D / 32], dv[4][D / 32];
+  clear<D>(dk);
+  clear<D>(dv);
+  const int rtiles = (a.Nq + kT - 1) / kT;
+  const long long all = (long long)R * G * rtiles;
+  const long long i0 = all * split / a.splits, i1 = k0 < count ? all * (split + 1) / a.splits : i0;
+  for (long long it = i0; it < i1; ++it) {
+    const int row0 = (int)(it % rtiles) * kT, rg = (int)(it / rtiles);
+    const int b = kb * R + rg / G, h = kh * G + rg % G;
+    __syncthreads();
+    load_tile<T, D>(sQ, static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h, a.qs.n, row0,
+                    [&](int r) { return row0 + r < a.Nq; });
+    load_tile<T, D>(sG, static_cast<const T*>(a.G) + b * a.gs.b + h * a.gs.h, a.gs.n, row0,
+                    [&](int r) { return row0 + r < a.Nq; });
+    load_rows(a, sL, sDelta, ((size_t)b * a.Hq + h) * a.Nq, row0);
+    __syncthreads();
+    float p[4][4], ds[4][4];
+    scores_back<D>(sQ, sG, sK, sV, sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sP[(ty + 16 * i) * kPS + tx + 16 * j] = p[i][j];
+        sD[(ty + 16 * i) * kPS + tx + 16 * j] = ds[i][j];
+      }
+    __syncthreads();
+    cols_cols<D>(sP, sG, ty, tx, dv);
+    cols_cols<D>(sD, sQ, ty, tx, dk);
+  }
+  const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = k0 + 4 * ty + i;
+    if (r >= a.Nk) continue;
+    const size_t at = (((size_t)kb * a.Hk + kh) * a.Nk + r) * D;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const float k4[4] = {dk[i][2 * c].x, dk[i][2 * c].y, dk[i][2 * c + 1].x, dk[i][2 * c + 1].y};
+      const float v4[4] = {dv[i][2 * c].x, dv[i][2 * c].y, dv[i][2 * c + 1].x, dv[i][2 * c + 1].y};
+      if (a.splits > 1) {
+        put4(a.part + (size_t)split * 2 * elems + at + 4 * tx + 64 * c, k4);
+        put4(a.part + ((size_t)split * 2 + 1) * elems + at + 4 * tx + 64 * c, v4);
+      } else {
+        put4(static_cast<T*>(a.dK) + at + 4 * tx + 64 * c, k4);
+        put4(static_cast<T*>(a.dV) + at + 4 * tx + 64 * c, v4);
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cross_simt_dq_kernel(const CrossArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float* sK = sm;
+  float* sV = sK + kT * pitch<D>();
+  float* sQ = sV + kT * pitch<D>();
+  float* sG = sQ + kT * pitch<D>();
+  float* sD = sG + kT * pitch<D>();
+  __shared__ float sL[kT], sDelta[kT];
+  __shared__ unsigned char seen[kT];
+  const int tiles = (a.Nq + kT - 1) / kT;
+  const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
+  const int b = bh / a.Hq, h = bh % a.Hq;
+  const int kb = b / (a.B / a.Bk), kh = h / (a.Hq / a.Hk);
+  const int row0 = rt * kT;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int count = key_count(a, kb);
+  const int ktiles = (count + kT - 1) / kT;
+  const int t0 = (int)((long long)ktiles * split / a.splits), t1 = (int)((long long)ktiles * (split + 1) / a.splits);
+  load_tile<T, D>(sQ, static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h, a.qs.n, row0,
+                  [&](int r) { return row0 + r < a.Nq; });
+  load_tile<T, D>(sG, static_cast<const T*>(a.G) + b * a.gs.b + h * a.gs.h, a.gs.n, row0,
+                  [&](int r) { return row0 + r < a.Nq; });
+  const size_t head_row = ((size_t)b * a.Hq + h) * a.Nq;
+  load_rows(a, sL, sDelta, head_row, row0);
+  const T* K = static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h;
+  const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
+  const float c2 = a.scale * kLog2e;
+  float2 dq[4][D / 32];
+  clear<D>(dq);
+  for (int t = t0; t < t1; ++t) {
+    const int k0 = t * kT;
+    __syncthreads();
+    if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
+    __syncthreads();
+    load_tile<T, D>(sK, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
+    load_tile<T, D>(sV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
+    __syncthreads();
+    float p[4][4], ds[4][4];
+    scores_back<D>(sQ, sG, sK, sV, sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sD[(ty + 16 * i) * kPS + tx + 16 * j] = ds[i][j];
+    __syncthreads();
+    rows_cols<D>(sD, sK, ty, tx, dq);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + ty + 16 * i;
+    if (r >= a.Nq) continue;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const float v[4] = {dq[i][2 * c].x, dq[i][2 * c].y, dq[i][2 * c + 1].x, dq[i][2 * c + 1].y};
+      const size_t at = (head_row + r) * D + 4 * tx + 64 * c;
+      if (a.splits > 1)
+        put4(a.part + (size_t)split * a.B * a.Hq * a.Nq * D + at, v);
+      else
+        put4(static_cast<T*>(a.dQ) + at, v);
+    }
+  }
+}
+
+template <typename F>
+cudaError_t with_smem(F* kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int D>
+cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)(3 * kT * pitch<D>() + kT * kPS) * sizeof(float);
+  cudaError_t e = with_smem(cross_simt_kernel<T, D>, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
+  cross_simt_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)(4 * kT * pitch<D>() + 2 * kT * kPS) * sizeof(float);
+  cudaError_t e = with_smem(cross_simt_dkv_kernel<T, D>, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT)), a.splits);
+  cross_simt_dkv_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)(4 * kT * pitch<D>() + kT * kPS) * sizeof(float);
+  cudaError_t e = with_smem(cross_simt_dq_kernel<T, D>, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
+  cross_simt_dq_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_simt(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log) {
+  log.add("cross_simt");
+  if (dt == AVQ_F32) return a.d == 64 ? forward<float, 64>(a, st) : forward<float, 128>(a, st);
+  return a.d == 64 ? forward<bf16, 64>(a, st) : forward<bf16, 128>(a, st);
+}
+cudaError_t launch_cross_simt_dkv(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log) {
+  log.add("cross_simt_dkv");
+  if (dt == AVQ_F32) return a.d == 64 ? dkv<float, 64>(a, st) : dkv<float, 128>(a, st);
+  return a.d == 64 ? dkv<bf16, 64>(a, st) : dkv<bf16, 128>(a, st);
+}
+cudaError_t launch_cross_simt_dq(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log) {
+  log.add("cross_simt_dq");
+  if (dt == AVQ_F32) return a.d == 64 ? dq<float, 64>(a, st) : dq<float, 128>(a, st);
+  return a.d == 64 ? dq<bf16, 64>(a, st) : dq<bf16, 128>(a, st);
+}
+
+}  // namespace avq

@@ -1,0 +1,422 @@
+// C ABI of the exact operators beside the quantised path (norms and rotation
+// of queries and keys, attention over another sequence): host-side validation
+// and dispatch.  Every check runs on the host before anything is enqueued.
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace avq {
+
+namespace {
+
+constexpr long long kMaxRows = 1ll << 30;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t elem(avq_dtype dt) { return dt == AVQ_F32 ? 4 : 2; }
+bool known(avq_dtype dt) { return dt == AVQ_F32 || dt == AVQ_BF16; }
+
+avq_status need_ptr(const void* p, const char* name) {
+  if (p == nullptr) return api_fail(AVQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(p, 16)) return api_fail(AVQ_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  return AVQ_OK;
+}
+
+// Strides of a [B,H,N,d] view, those of dimensions of size 1 set to 0; the
+// tensor's extent in bytes in *span.
+avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, bool output, const char* name,
+                Strides* out, size_t* span) {
+  if (s == nullptr) return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides are NULL", name);
+  const int64_t v[3] = {B > 1 ? s->b : 0, H > 1 ? s->h : 0, N > 1 ? s->n : 0};
+  const int n[3] = {B, H, N};
+  const int64_t es = (int64_t)elem(dt);
+  int64_t last = d;
+  for (int i = 0; i < 3; ++i) {
+    if (v[i] < 0 || v[i] > (int64_t)1 << 40)
+      return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", name);
+    if (v[i] * es % 16 != 0)
+      return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", name);
+    if (output && n[i] > 1 && v[i] < d)
+      return api_fail(AVQ_ERR_INVALID_ARG, "%s: an output's heads must not overlap", name);
+    last += v[i] * (int64_t)(n[i] > 0 ? n[i] - 1 : 0);
+  }
+  *out = Strides{v[0], v[1], v[2]};
+  if (span != nullptr) *span = (size_t)(last * es);
+  return AVQ_OK;
+}
+
+bool overlap(const void* x, size_t xn, const void* y, size_t yn) {
+  const char *a = static_cast<const char*>(x), *b = static_cast<const char*>(y);
+  return a < b + yn && b < a + xn;
+}
+
+avq_status check_ws(size_t need, const void* ws, size_t bytes) {
+  if (need == 0) return AVQ_OK;
+  if (ws == nullptr || bytes < need)
+    return api_fail(AVQ_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu at %p)", need, bytes, ws);
+  if (!aligned(ws, 256)) return api_fail(AVQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return AVQ_OK;
+}
+
+#define AVQ_TRY(call)                       \
+  do {                                      \
+    const avq_status try_st = (call);       \
+    if (try_st != AVQ_OK) return try_st;    \
+  } while (0)
+
+// ---- norms and rotation ------------------------------------------------------
+
+avq_status check_qk(const avq_qk_dims* s, avq_dtype dt) {
+  if (s == nullptr) return api_fail(AVQ_ERR_INVALID_ARG, "dims is NULL");
+  if (!known(dt)) return api_fail(AVQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+  if (s->B < 1 || s->N < 1 || s->Hq < 1 || s->Hk < 0)
+    return api_fail(AVQ_ERR_INVALID_ARG, "B, N and Hq must be >= 1 and Hk >= 0 (got %d, %d, %d, %d)", s->B, s->N,
+                    s->Hq, s->Hk);
+  if (s->d != 64 && s->d != 128) return api_fail(AVQ_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", s->d);
+  const long long tokens = (long long)s->B * s->N;
+  if (tokens >= kMaxRows || tokens * s->Hq >= kMaxRows || tokens * s->Hk >= kMaxRows)
+    return api_fail(AVQ_ERR_UNSUPPORTED, "B*H*N must be below 2^30");
+  if (s->axes != 1 && s->axes != 2) return api_fail(AVQ_ERR_INVALID_ARG, "axes must be 1 or 2 (got %d)", s->axes);
+  if (s->rot < 0 || s->rot > s->d || s->rot % (8 * s->axes) != 0)
+    return api_fail(AVQ_ERR_INVALID_ARG, "rot must be a multiple of %d in [0, d] (got %d)", 8 * s->axes, s->rot);
+  if (s->layout != AVQ_ROTARY_HALF && s->layout != AVQ_ROTARY_INTERLEAVED)
+    return api_fail(AVQ_ERR_INVALID_ARG, "unknown rotary layout %d", s->layout);
+  if (s->norm < AVQ_NORM_NONE || s->norm > AVQ_NORM_LAYER)
+    return api_fail(AVQ_ERR_INVALID_ARG, "unknown norm %d", s->norm);
+  if (!(s->eps >= 0.f) || !isfinite(s->eps)) return api_fail(AVQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!isfinite(s->mscale)) return api_fail(AVQ_ERR_INVALID_ARG, "mscale must be finite");
+  return AVQ_OK;
+}
+
+avq_status check_turn(const avq_qk_dims& s, const int32_t* positions, const double* freqs) {
+  if (s.rot == 0) return AVQ_OK;
+  if (!aligned(positions, 4)) return api_fail(AVQ_ERR_INVALID_ARG, "positions is not 4-byte aligned");
+  if (freqs == nullptr) return api_fail(AVQ_ERR_INVALID_ARG, "freqs is NULL");
+  if (!aligned(freqs, 8)) return api_fail(AVQ_ERR_INVALID_ARG, "freqs is not 8-byte aligned");
+  return AVQ_OK;
+}
+
+avq_status optional_vector(const void* p, const char* name) {
+  return p == nullptr ? AVQ_OK : need_ptr(p, name);
+}
+
+struct Pair {
+  const void* x[2];
+  Strides s[2];
+  size_t span[2];
+};
+avq_status pair_of(const avq_qk_dims& s, avq_dtype dt, const void* q, const avq_strides* qs, const char* qn,
+                   const void* k, const avq_strides* ks, const char* kn, Pair* out) {
+  *out = Pair{};
+  AVQ_TRY(need_ptr(q, qn));
+  AVQ_TRY(view(qs, s.B, s.Hq, s.N, s.d, dt, false, qn, &out->s[0], &out->span[0]));
+  out->x[0] = q;
+  if (s.Hk > 0) {
+    AVQ_TRY(need_ptr(k, kn));
+    AVQ_TRY(view(ks, s.B, s.Hk, s.N, s.d, dt, false, kn, &out->s[1], &out->span[1]));
+    out->x[1] = k;
+  }
+  return AVQ_OK;
+}
+// Dense outputs, apart from each other and from the inputs.
+avq_status outputs_of(const avq_qk_dims& s, avq_dtype dt, void* q, const char* qn, void* k, const char* kn,
+                      const Pair* ins, int count, void** out) {
+  AVQ_TRY(need_ptr(q, qn));
+  out[0] = q;
+  out[1] = nullptr;
+  if (s.Hk > 0) {
+    AVQ_TRY(need_ptr(k, kn));
+    out[1] = k;
+  }
+  const size_t bytes[2] = {(size_t)s.B * s.Hq * s.N * s.d * elem(dt), (size_t)s.B * s.Hk * s.N * s.d * elem(dt)};
+  const char* names[2] = {qn, kn};
+  for (int o = 0; o < (s.Hk > 0 ? 2 : 1); ++o)
+    for (int i = 0; i < count; ++i)
+      for (int w = 0; w < (s.Hk > 0 ? 2 : 1); ++w)
+        if (overlap(out[o], bytes[o], ins[i].x[w], ins[i].span[w]))
+          return api_fail(AVQ_ERR_INVALID_ARG, "%s overlaps an input", names[o]);
+  if (s.Hk > 0 && overlap(q, bytes[0], k, bytes[1])) return api_fail(AVQ_ERR_INVALID_ARG, "%s and %s overlap", qn, kn);
+  return AVQ_OK;
+}
+
+// ---- attention over another sequence -------------------------------------------
+
+avq_status check_cross(const avq_cross_dims* s, avq_dtype dt) {
+  if (s == nullptr) return api_fail(AVQ_ERR_INVALID_ARG, "dims is NULL");
+  if (!known(dt)) return api_fail(AVQ_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+  if (s->B < 1 || s->Bk < 1 || s->Hq < 1 || s->Hk < 1 || s->Nq < 1 || s->Nk < 0)
+    return api_fail(AVQ_ERR_INVALID_ARG, "B, Bk, Hq, Hk and Nq must be >= 1 and Nk >= 0");
+  if (s->B % s->Bk != 0) return api_fail(AVQ_ERR_INVALID_ARG, "B must be a multiple of Bk (got %d, %d)", s->B, s->Bk);
+  if (s->Hq % s->Hk != 0)
+    return api_fail(AVQ_ERR_INVALID_ARG, "Hq must be a multiple of Hk (got %d, %d)", s->Hq, s->Hk);
+  if (s->d != 64 && s->d != 128) return api_fail(AVQ_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", s->d);
+  const long long qh = (long long)s->B * s->Hq, kh = (long long)s->Bk * s->Hk;
+  if (qh >= kMaxRows || qh * s->Nq >= kMaxRows || kh >= kMaxRows || kh * s->Nk >= kMaxRows)
+    return api_fail(AVQ_ERR_UNSUPPORTED, "B*Hq*Nq and Bk*Hk*Nk must be below 2^30");
+  if (!(s->scale > 0.f) || !isfinite(s->scale)) return api_fail(AVQ_ERR_INVALID_ARG, "scale must be finite and > 0");
+  return AVQ_OK;
+}
+
+// Ranges of the long axis (`units` tiles of it) when `items` blocks alone
+// would leave SMs idle: as many as bring the blocks to `target`, none shorter
+// than one tile.
+int split_count(long long items, long long units, long long target) {
+  long long n = items >= target ? 1 : target / items;
+  if (n > units) n = units;
+  if (n > 64) n = 64;
+  return n < 1 ? 1 : (int)n;
+}
+long long tiles64(long long n) { return (n + 63) / 64; }
+
+// How a call is carried out, from its sizes, type and path alone.
+struct CrossPlan {
+  int splits = 1;  // forward
+  int dkv_splits = 1, dq_splits = 1;
+  size_t part = 0, part_lse = 0, delta = 0;  // bytes, each a multiple of 256
+  size_t total() const { return part + part_lse + delta; }
+};
+
+CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
+  CrossPlan p;
+  const long long target = 2ll * num_sms();
+  const long long rows = (long long)s.B * s.Hq * s.Nq, keys = (long long)s.Bk * s.Hk * s.Nk;
+  const long long row_items = (long long)s.B * s.Hq * tiles64(s.Nq), key_items = (long long)s.Bk * s.Hk * tiles64(s.Nk);
+  const long long row_units = (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * tiles64(s.Nq);
+  if (!backward) {
+    p.splits = split_count(row_items, tiles64(s.Nk), target);
+    if (p.splits > 1) {
+      p.part = up256((size_t)p.splits * rows * s.d * 4);
+      p.part_lse = up256((size_t)p.splits * rows * 4);
+    }
+    return p;
+  }
+  p.delta = up256((size_t)rows * 4);
+  p.dq_splits = split_count(row_items, tiles64(s.Nk), target);
+  if (key_items > 0) p.dkv_splits = split_count(key_items, row_units, target);
+  // dK and dV, then dQ, one after the other in the same place
+  const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * rows * s.d * 4 : 0;
+  const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * keys * s.d * 4 : 0;
+  p.part = up256(dq > dkv ? dq : dkv);
+  return p;
+}
+
+avq_status cross_inputs(const avq_cross_dims& s, avq_dtype dt, const void* Q, const avq_strides* qs, const void* K,
+                        const avq_strides* ks, const void* V, const avq_strides* vs, const int32_t* kv_lens,
+                        const uint8_t* key_mask, CrossArgs* a, size_t* spans) {
+  AVQ_TRY(need_ptr(Q, "Q"));
+  AVQ_TRY(view(qs, s.B, s.Hq, s.Nq, s.d, dt, false, "Q", &a->qs, &spans[0]));
+  if (s.Nk > 0) {
+    AVQ_TRY(need_ptr(K, "K"));
+    AVQ_TRY(need_ptr(V, "V"));
+    AVQ_TRY(view(ks, s.Bk, s.Hk, s.Nk, s.d, dt, false, "K", &a->ks, &spans[1]));
+    AVQ_TRY(view(vs, s.Bk, s.Hk, s.Nk, s.d, dt, false, "V", &a->vs, &spans[2]));
+  } else {
+    spans[1] = spans[2] = 0;
+  }
+  if (!aligned(kv_lens, 4)) return api_fail(AVQ_ERR_INVALID_ARG, "kv_lens is not 4-byte aligned");
+  a->B = s.B, a->Bk = s.Bk, a->Hq = s.Hq, a->Hk = s.Hk, a->Nq = s.Nq, a->Nk = s.Nk, a->d = s.d;
+  a->scale = s.scale;
+  a->splits = 1;
+  a->Q = Q, a->K = K, a->V = V;
+  a->kv_lens = kv_lens, a->key_mask = key_mask;
+  return AVQ_OK;
+}
+
+}  // namespace
+}  // namespace avq
+
+using namespace avq;
+
+extern "C" {
+
+avq_status avq_rotary(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, const avq_strides* q_strides,
+                      const void* K, const avq_strides* k_strides, const int32_t* positions, const double* freqs,
+                      int inverse, void* Yq, void* Yk, avq_stream_t stream) {
+  api_begin();
+  AVQ_TRY(check_qk(dims, dtype));
+  if (dims->norm != AVQ_NORM_NONE) return api_fail(AVQ_ERR_INVALID_ARG, "norm must be AVQ_NORM_NONE");
+  AVQ_TRY(check_turn(*dims, positions, freqs));
+  Pair in;
+  void* out[2];
+  AVQ_TRY(pair_of(*dims, dtype, Q, q_strides, "Q", K, k_strides, "K", &in));
+  AVQ_TRY(outputs_of(*dims, dtype, Yq, "Yq", Yk, "Yk", &in, 1, out));
+  if (api_injected("rotary")) return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_rotary)");
+  const void* none[2] = {nullptr, nullptr};
+  LaunchLog log{};
+  const cudaError_t e = launch_qk_norm(*dims, dtype, in.x, in.s, none, none, positions, freqs, inverse != 0, out,
+                                       reinterpret_cast<cudaStream_t>(stream), log);
+  return api_finish(e, "rotary launch", log);
+}
+
+avq_status avq_qk_norm(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, const avq_strides* q_strides,
+                       const void* K, const avq_strides* k_strides, const void* wq, const void* wk, const void* bq,
+                       const void* bk, const int32_t* positions, const double* freqs, void* Yq, void* Yk,
+                       avq_stream_t stream) {
+  api_begin();
+  AVQ_TRY(check_qk(dims, dtype));
+  if (dims->norm == AVQ_NORM_NONE) return api_fail(AVQ_ERR_INVALID_ARG, "norm must be RMS or LAYER");
+  AVQ_TRY(check_turn(*dims, positions, freqs));
+  Pair in;
+  void* out[2];
+  AVQ_TRY(pair_of(*dims, dtype, Q, q_strides, "Q", K, k_strides, "K", &in));
+  AVQ_TRY(optional_vector(wq, "wq"));
+  AVQ_TRY(optional_vector(wk, "wk"));
+  AVQ_TRY(optional_vector(bq, "bq"));
+  AVQ_TRY(optional_vector(bk, "bk"));
+  AVQ_TRY(outputs_of(*dims, dtype, Yq, "Yq", Yk, "Yk", &in, 1, out));
+  if (api_injected("qk_norm")) return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_qk_norm)");
+  const void* w[2] = {wq, wk};
+  const void* b[2] = {bq, bk};
+  LaunchLog log{};
+  const cudaError_t e = launch_qk_norm(*dims, dtype, in.x, in.s, w, b, positions, freqs, false, out,
+                                       reinterpret_cast<cudaStream_t>(stream), log);
+  return api_finish(e, "qk_norm launch", log);
+}
+
+size_t avq_qk_norm_workspace_size(const avq_qk_dims* dims, avq_dtype dtype) {
+  if (dims == nullptr || dims->B < 1 || dims->N < 1 || !known(dtype) || (dims->d != 64 && dims->d != 128)) return 0;
+  if ((long long)dims->B * dims->N >= kMaxRows) return 0;
+  return up256(qk_norm_backward_workspace(*dims));
+}
+
+avq_status avq_qk_norm_backward(const avq_qk_dims* dims, avq_dtype dtype, const void* dYq,
+                                const avq_strides* dyq_strides, const void* dYk, const avq_strides* dyk_strides,
+                                const void* Q, const avq_strides* q_strides, const void* K,
+                                const avq_strides* k_strides, const void* wq, const void* wk,
+                                const int32_t* positions, const double* freqs, void* dQ, void* dK, float* dwq,
+                                float* dwk, float* dbq, float* dbk, void* ws, size_t ws_bytes,
+                                avq_stream_t stream) {
+  api_begin();
+  AVQ_TRY(check_qk(dims, dtype));
+  if (dims->norm == AVQ_NORM_NONE) return api_fail(AVQ_ERR_INVALID_ARG, "norm must be RMS or LAYER");
+  AVQ_TRY(check_turn(*dims, positions, freqs));
+  Pair in[2];
+  void* out[2];
+  AVQ_TRY(pair_of(*dims, dtype, dYq, dyq_strides, "dYq", dYk, dyk_strides, "dYk", &in[0]));
+  AVQ_TRY(pair_of(*dims, dtype, Q, q_strides, "Q", K, k_strides, "K", &in[1]));
+  AVQ_TRY(optional_vector(wq, "wq"));
+  AVQ_TRY(optional_vector(wk, "wk"));
+  AVQ_TRY(outputs_of(*dims, dtype, dQ, "dQ", dK, "dK", in, 2, out));
+  AVQ_TRY(optional_vector(dwq, "dwq"));
+  AVQ_TRY(optional_vector(dwk, "dwk"));
+  AVQ_TRY(optional_vector(dbq, "dbq"));
+  AVQ_TRY(optional_vector(dbk, "dbk"));
+  AVQ_TRY(check_ws(up256(qk_norm_backward_workspace(*dims)), ws, ws_bytes));
+  if (api_injected("qk_norm_backward"))
+    return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_qk_norm_backward)");
+  const void* w[2] = {wq, wk};
+  float* dw[2] = {dwq, dims->Hk > 0 ? dwk : nullptr};
+  float* db[2] = {dbq, dims->Hk > 0 ? dbk : nullptr};
+  LaunchLog log{};
+  const cudaError_t e = launch_qk_norm_backward(*dims, dtype, in[0].x, in[0].s, in[1].x, in[1].s, w, positions, freqs,
+                                                out, dw, db, ws, reinterpret_cast<cudaStream_t>(stream), log);
+  return api_finish(e, "qk_norm_backward launch", log);
+}
+
+size_t avq_cross_workspace_size(const avq_cross_dims* dims, avq_dtype dtype, int backward) {
+  api_begin();
+  if (check_cross(dims, dtype) != AVQ_OK) return 0;
+  return plan_cross(*dims, dtype, backward != 0).total();
+}
+
+avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, const void* Q,
+                               const avq_strides* q_strides, const void* K, const avq_strides* k_strides,
+                               const void* V, const avq_strides* v_strides, const int32_t* kv_lens,
+                               const uint8_t* key_mask, void* O, const avq_strides* o_strides, float* lse, void* ws,
+                               size_t ws_bytes, avq_stream_t stream) {
+  api_begin();
+  AVQ_TRY(check_cross(dims, dtype));
+  const avq_cross_dims& s = *dims;
+  CrossArgs a{};
+  size_t spans[3], ospan;
+  AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
+  AVQ_TRY(need_ptr(O, "O"));
+  AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, true, "O", &a.os, &ospan));
+  const void* ins[3] = {Q, K, V};
+  for (int i = 0; i < 3; ++i)
+    if (spans[i] > 0 && overlap(O, ospan, ins[i], spans[i])) return api_fail(AVQ_ERR_INVALID_ARG, "O overlaps an input");
+  AVQ_TRY(optional_vector(lse, "lse"));
+  const CrossPlan p = plan_cross(s, dtype, false);
+  AVQ_TRY(check_ws(p.total(), ws, ws_bytes));
+  if (api_path() == AVQ_PATH_TC && dtype != AVQ_BF16)
+    return api_fail(AVQ_ERR_UNSUPPORTED, "no tensor-core kernel for this type");
+  if (api_injected("cross_attention"))
+    return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_cross_attention)");
+  a.O = O;
+  a.lse = lse;
+  a.splits = p.splits;
+  a.part = static_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log{};
+  cudaError_t e = launch_cross_simt(a, dtype, cs, log);
+  if (e == cudaSuccess && a.splits > 1) e = launch_cross_join(a, dtype, cs, log);
+  return api_finish(e, "cross attention launch", log);
+}
+
+avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dtype, const void* dO,
+                                        const avq_strides* do_strides, const void* Q, const avq_strides* q_strides,
+                                        const void* K, const avq_strides* k_strides, const void* V,
+                                        const avq_strides* v_strides, const void* O, const avq_strides* o_strides,
+                                        const float* lse, const int32_t* kv_lens, const uint8_t* key_mask, void* dQ,
+                                        void* dK, void* dV, void* ws, size_t ws_bytes, avq_stream_t stream) {
+  api_begin();
+  AVQ_TRY(check_cross(dims, dtype));
+  const avq_cross_dims& s = *dims;
+  CrossArgs a{};
+  size_t spans[5];
+  AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
+  AVQ_TRY(need_ptr(dO, "dO"));
+  AVQ_TRY(view(do_strides, s.B, s.Hq, s.Nq, s.d, dtype, false, "dO", &a.gs, &spans[3]));
+  AVQ_TRY(need_ptr(O, "O"));
+  AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, false, "O", &a.os, &spans[4]));
+  AVQ_TRY(need_ptr(lse, "lse"));
+  AVQ_TRY(need_ptr(dQ, "dQ"));
+  if (s.Nk > 0) {
+    AVQ_TRY(need_ptr(dK, "dK"));
+    AVQ_TRY(need_ptr(dV, "dV"));
+  }
+  const size_t qn = (size_t)s.B * s.Hq * s.Nq * s.d, kn = (size_t)s.Bk * s.Hk * s.Nk * s.d;
+  const void* ins[5] = {Q, K, V, dO, O};
+  const void* outs[3] = {dQ, dK, dV};
+  const size_t bytes[3] = {qn * elem(dtype), kn * elem(dtype), kn * elem(dtype)};
+  for (int o = 0; o < (s.Nk > 0 ? 3 : 1); ++o) {
+    for (int i = 0; i < 5; ++i)
+      if (spans[i] > 0 && overlap(outs[o], bytes[o], ins[i], spans[i]))
+        return api_fail(AVQ_ERR_INVALID_ARG, "a gradient overlaps an input");
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[o], bytes[o], outs[i], bytes[i])) return api_fail(AVQ_ERR_INVALID_ARG, "gradients overlap");
+  }
+  const CrossPlan p = plan_cross(s, dtype, true);
+  AVQ_TRY(check_ws(p.total(), ws, ws_bytes));
+  if (api_path() == AVQ_PATH_TC && dtype != AVQ_BF16)
+    return api_fail(AVQ_ERR_UNSUPPORTED, "no tensor-core kernel for this type");
+  if (api_injected("cross_attention_backward"))
+    return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_cross_attention_backward)");
+  a.G = dO;
+  a.O = const_cast<void*>(O);
+  a.lse = const_cast<float*>(lse);
+  a.dQ = dQ, a.dK = dK, a.dV = dV;
+  a.part = static_cast<float*>(ws);
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log{};
+  cudaError_t e = launch_cross_delta(a, dtype, cs, log);
+  if (e == cudaSuccess && s.Nk > 0) {
+    a.splits = p.dkv_splits;
+    e = launch_cross_simt_dkv(a, dtype, cs, log);
+    if (a.splits > 1) {
+      if (e == cudaSuccess) e = launch_partial_sum(dtype, a.part, 2 * kn, a.splits, dK, kn, cs, log);
+      if (e == cudaSuccess) e = launch_partial_sum(dtype, a.part + kn, 2 * kn, a.splits, dV, kn, cs, log);
+    }
+  }
+  if (e == cudaSuccess) {
+    a.splits = p.dq_splits;
+    e = launch_cross_simt_dq(a, dtype, cs, log);
+    if (e == cudaSuccess && a.splits > 1) e = launch_partial_sum(dtype, a.part, qn, a.splits, dQ, qn, cs, log);
+  }
+  return api_finish(e, "cross attention backward launch", log);
+}
+
+}  // extern "C"

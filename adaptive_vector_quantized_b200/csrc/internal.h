@@ -118,6 +118,53 @@ cudaError_t launch_permute(const void* X, const int32_t* idx, void* Y, int batch
 cudaError_t make_tmap_3d_bf16(CUtensorMap* map, const void* base, int inner, int rows, int batch,
                               int box_inner, int box_rows);
 
+// ---- exact attention beside the quantised path -----------------------------
+typedef avq_strides Strides;
+
+// Queries or keys [B][H][N][d] as x[0], x[1] (rotation alone when s.norm is
+// AVQ_NORM_NONE; `inverse` turns the other way).
+cudaError_t launch_qk_norm(const avq_qk_dims& s, avq_dtype dt, const void* const* x, const Strides* xs,
+                           const void* const* w, const void* const* b, const int32_t* pos, const double* freqs,
+                           bool inverse, void* const* y, cudaStream_t st, LaunchLog& log);
+size_t qk_norm_backward_workspace(const avq_qk_dims& s);
+cudaError_t launch_qk_norm_backward(const avq_qk_dims& s, avq_dtype dt, const void* const* g, const Strides* gs,
+                                    const void* const* x, const Strides* xs, const void* const* w,
+                                    const int32_t* pos, const double* freqs, void* const* dx, float* const* dw,
+                                    float* const* db, void* ws, cudaStream_t st, LaunchLog& log);
+
+// Everything the cross attention's kernels read and write.  splits: ranges
+// of the long axis (keys, or query rows for dK and dV) whose partial results
+// go to `part` (and `part_lse`) in fp32 and are joined by a launch of their own.
+struct CrossArgs {
+  int B, Bk, Hq, Hk, Nq, Nk, d;
+  float scale;
+  int splits;
+  Strides qs, ks, vs, os, gs;
+  const void *Q, *K, *V, *G;  // G: the gradient of O
+  void *O, *dQ, *dK, *dV;
+  float *lse, *delta, *part, *part_lse;
+  const int32_t* kv_lens;
+  const uint8_t* key_mask;
+};
+cudaError_t launch_cross_simt(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+cudaError_t launch_cross_simt_dkv(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+cudaError_t launch_cross_simt_dq(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+// Joins the forward pass's partial results (softmaxes over disjoint keys).
+cudaError_t launch_cross_join(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+// out[i] = sum over s < splits of part[s * stride + i], i < n (a multiple of 4).
+cudaError_t launch_partial_sum(avq_dtype dt, const float* part, size_t stride, int splits, void* out, size_t n,
+                               cudaStream_t st, LaunchLog& log);
+// delta = rowsum(dO O)
+cudaError_t launch_cross_delta(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+
+// What the entry points outside avq_api.cu share with it: the thread-local
+// error text, kernel names and path, and the injected failures.
+avq_status api_begin();
+avq_status api_fail(avq_status s, const char* fmt, ...);
+avq_status api_finish(cudaError_t e, const char* where, const LaunchLog& log);
+int api_path();
+bool api_injected(const char* entry);
+
 // Device address of the current device's error word.
 unsigned int* error_word();
 // One thread waits, with the given limit, on an mbarrier that nothing

@@ -25,7 +25,9 @@
  *     the device error word and reported by avq_check_device.
  *   - Fault injection for tests of a caller's error handling: if the
  *     environment variable AVQ_FAULT is "quantize", "attention",
- *     "codebook_update", "permute" or "all", the named entry points return
+ *     "codebook_update", "permute", "rotary", "qk_norm", "qk_norm_backward",
+ *     "cross_attention", "cross_attention_backward" or "all", the named entry
+ *     points return
  *     AVQ_ERR_CUDA after their argument checks, before any launch (nothing
  *     reaches the GPU).  Unset or empty: no effect.
  *   - Layouts are dense row-major.  BH = B*H; tensor [B,H,N,d] puts head
@@ -324,6 +326,166 @@ avq_status avq_hilbert_order(int side, int32_t* idx);
  * non-positive size, width*height > INT32_MAX or a NULL idx.
  */
 avq_status avq_gilbert_order(int width, int height, int32_t* idx);
+
+/* ---- exact attention beside the quantised path ---------------------------
+ *
+ * The models that hold an AVQ layer also normalise queries and keys (Sec. F
+ * puts a LayerNorm on the keys before they are quantised), turn them by
+ * their positions, and attend over another sequence (the text states of a
+ * diffusion model's blocks, Sec. 5.4).  The calls below do that work in the
+ * layouts of avq_quantize and avq_attention, with the gradients that
+ * training needs.  Inputs may be views: a tensor [B,H,N,d] is given by its
+ * address and avq_strides, so that the heads of a joint projection's output
+ * are read in place.  Outputs are dense unless strides are taken for them.
+ */
+
+/* Strides, in elements, of batch entry, head and token of a [B,H,N,d] tensor
+ * whose last dimension is contiguous.  Each times the element size must be a
+ * multiple of 16 bytes, and none negative (0 repeats the same data; not for
+ * outputs).  The stride of a dimension of size 1 is not used. */
+typedef struct {
+  int64_t b, h, n;
+} avq_strides;
+
+typedef enum { AVQ_NORM_NONE = 0, AVQ_NORM_RMS = 1, AVQ_NORM_LAYER = 2 } avq_norm;
+/* Which elements of a head form pair i of rot / 2: (i, i + rot/2) or (2i, 2i+1). */
+typedef enum { AVQ_ROTARY_HALF = 0, AVQ_ROTARY_INTERLEAVED = 1 } avq_rotary_layout;
+
+/* Queries [B,Hq,N,d] and keys [B,Hk,N,d] of one layer; Hk may be 0 (queries
+ * only).  rot: leading elements of each head that are rotated, a multiple of
+ * 8 (of 16 with axes == 2) in [0, d]; 0: no rotation.  axes: 1, or 2 for
+ * tokens of a grid: the first half of the pairs turns by a token's first
+ * position, the second half by its second.  pos_batch: positions are given
+ * per batch entry.  norm: avq_norm; eps >= 0 is added to the mean square (RMS)
+ * or the variance (LayerNorm).  layout: avq_rotary_layout.  mscale: factor on
+ * sine and cosine.  d in {64, 128}; B*Hq*N and B*Hk*N < 2^30. */
+typedef struct {
+  int B, N, Hq, Hk, d;
+  int rot, axes, pos_batch, layout, norm;
+  float eps, mscale;
+} avq_qk_dims;
+
+/*
+ * avq_rotary -- rotation of queries and keys by position.
+ * Pair i of token n turns by the angle positions[n] * freqs[i]; elements past
+ * rot are copied.  Angles are formed and reduced in 64 bits, so far positions
+ * lose nothing.
+ * Inputs (device): Q, K of `dtype` with strides; positions int32 [N] or
+ * [B,N], with axes == 2 [N,2] or [B,N,2] (NULL: 0..N-1; with axes == 2 both
+ * positions of a token are then n); freqs fp64 [rot/2], as avq_rotary_freqs
+ * makes them.  inverse != 0 turns the other way (mscale stays a factor): the
+ * gradient of the forward call.  dims->norm must be AVQ_NORM_NONE.
+ * Outputs: Yq [B,Hq,N,d], Yk [B,Hk,N,d], dense, not overlapping the inputs.
+ * K, Yk and k_strides are ignored when Hk == 0.
+ */
+avq_status avq_rotary(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, const avq_strides* q_strides,
+                      const void* K, const avq_strides* k_strides, const int32_t* positions,
+                      const double* freqs, int inverse, void* Yq, void* Yk, avq_stream_t stream);
+
+/*
+ * avq_qk_norm -- norm of every query and key head, then the rotation, in one
+ * pass: y = R(u w + b) with u = x / sqrt(mean(x^2) + eps) (RMS) or
+ * (x - mean(x)) / sqrt(var(x) + eps) (LayerNorm), R as in avq_rotary (rot == 0:
+ * none; positions and freqs are then ignored).
+ * wq, wk: weights [d] of `dtype`, shared by the heads, or NULL (1); bq, bk:
+ * biases [d] or NULL (0).  Arithmetic is fp32, rounded once at the end.
+ */
+avq_status avq_qk_norm(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, const avq_strides* q_strides,
+                       const void* K, const avq_strides* k_strides, const void* wq, const void* wk,
+                       const void* bq, const void* bk, const int32_t* positions, const double* freqs,
+                       void* Yq, void* Yk, avq_stream_t stream);
+
+/*
+ * avq_qk_norm_backward -- gradients of avq_qk_norm.
+ * Inputs: dYq, dYk, the gradients of its outputs, and its inputs Q, K, each
+ * with strides; wq, wk as given to it.  Outputs: dQ [B,Hq,N,d], dK [B,Hk,N,d]
+ * of `dtype`, dense; dwq, dwk, dbq, dbk fp32 [d], each may be NULL.  Nothing
+ * is kept by the forward pass: u is recomputed.  The weight gradients are
+ * summed in a fixed order: the same from run to run on one kind of GPU.
+ * Workspace: avq_qk_norm_workspace_size(dims, dtype) bytes, 256-byte aligned.
+ */
+avq_status avq_qk_norm_backward(const avq_qk_dims* dims, avq_dtype dtype, const void* dYq,
+                                const avq_strides* dyq_strides, const void* dYk, const avq_strides* dyk_strides,
+                                const void* Q, const avq_strides* q_strides, const void* K,
+                                const avq_strides* k_strides, const void* wq, const void* wk,
+                                const int32_t* positions, const double* freqs, void* dQ, void* dK, float* dwq,
+                                float* dwk, float* dbq, float* dbk, void* ws, size_t ws_bytes,
+                                avq_stream_t stream);
+size_t avq_qk_norm_workspace_size(const avq_qk_dims* dims, avq_dtype dtype);
+
+/* How avq_rotary_freqs stretches positions beyond the trained range. */
+typedef enum {
+  AVQ_ROTARY_PLAIN = 0,  /* base^(-i/pairs)                                           */
+  AVQ_ROTARY_LINEAR = 1, /* all frequencies divided by factor (interpolated positions) */
+  AVQ_ROTARY_NTK = 2,    /* base times factor^(pairs/(pairs-1)): the slowest pair is
+                            divided by factor, the fastest kept                       */
+  AVQ_ROTARY_YARN = 3    /* pairs that turn fewer than turns_low times over the trained
+                            range divided by factor, those above turns_high kept, a
+                            linear ramp over the pairs between; mscale 0.1 ln(factor) + 1 */
+} avq_rotary_scaling;
+
+/*
+ * avq_rotary_freqs -- host helper: frequencies (radians per position) of the
+ * rot / 2 pairs and the factor on sine and cosine (1 except for YARN).  With
+ * axes == 2 each axis has rot / 4 pairs with the frequencies of a rotation of
+ * rot / 2 elements.  freqs is host memory of rot / 2 doubles; mscale of one
+ * float (may be NULL).  base > 1; factor >= 1; trained >= 1 and
+ * 0 < turns_low < turns_high matter for YARN only.
+ */
+avq_status avq_rotary_freqs(int rot, int axes, double base, avq_rotary_scaling scaling, double factor,
+                            int trained, double turns_low, double turns_high, double* freqs, float* mscale);
+
+/* Attention of queries [B,Hq,Nq,d] over another sequence's keys and values
+ * [Bk,Hk,Nk,d].  Hq must be a multiple of Hk: query head h reads key head
+ * h / (Hq/Hk).  B must be a multiple of Bk: batch entry b reads encoder
+ * sequence b / (B/Bk), so that samples or beams drawn from one sequence read
+ * its states once.  scale > 0, finite.  d in {64, 128}; Nq >= 1; Nk >= 0;
+ * B*Hq*Nq and Bk*Hk*Nk < 2^30. */
+typedef struct {
+  int B, Bk, Hq, Hk, Nq, Nk, d;
+  float scale;
+} avq_cross_dims;
+
+/*
+ * avq_cross_attention -- exact softmax attention (Eq. 1) over another sequence:
+ *   S = scale Q K^T over the keys that are looked at, O = softmax(S) V,
+ *   lse = log sum exp(S).
+ * Looked at are the keys below kv_lens[kb] (int32 [Bk], NULL: Nk; values
+ * outside [0, Nk] are taken as the nearer end) whose key_mask byte (uint8
+ * [Bk,Nk], NULL: all) is not 0.  What stands in the others' K and V does not
+ * matter, infinities and NaN included.  A row with no key gives O = 0 and
+ * lse = -inf.
+ * Outputs (device): O [B,Hq,Nq,d] of `dtype` with strides; lse fp32
+ * [B,Hq,Nq], dense, or NULL.  O overlaps no input.
+ * Workspace: avq_cross_workspace_size(dims, dtype, 0) bytes, 256-byte
+ * aligned; NULL when that is 0.  It depends on the kernel family
+ * (avq_set_path) in force, as the call does.
+ */
+avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, const void* Q,
+                               const avq_strides* q_strides, const void* K, const avq_strides* k_strides,
+                               const void* V, const avq_strides* v_strides, const int32_t* kv_lens,
+                               const uint8_t* key_mask, void* O, const avq_strides* o_strides, float* lse,
+                               void* ws, size_t ws_bytes, avq_stream_t stream);
+
+/*
+ * avq_cross_attention_backward -- gradients of avq_cross_attention.
+ * Inputs: dO with strides; Q, K, V, kv_lens, key_mask as given to the forward
+ * call, and the O (with strides) and lse that it wrote.
+ * Outputs: dQ [B,Hq,Nq,d]; dK, dV [Bk,Hk,Nk,d], summed over the query heads
+ * and batch entries that share them; of `dtype`, dense, written in full (keys
+ * that are not looked at get 0).  No atomics: results are the same from run
+ * to run on one kind of GPU.
+ * Workspace: avq_cross_workspace_size(dims, dtype, 1) bytes.
+ */
+avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dtype, const void* dO,
+                                        const avq_strides* do_strides, const void* Q,
+                                        const avq_strides* q_strides, const void* K,
+                                        const avq_strides* k_strides, const void* V,
+                                        const avq_strides* v_strides, const void* O,
+                                        const avq_strides* o_strides, const float* lse, const int32_t* kv_lens,
+                                        const uint8_t* key_mask, void* dQ, void* dK, void* dV, void* ws,
+                                        size_t ws_bytes, avq_stream_t stream);
+size_t avq_cross_workspace_size(const avq_cross_dims* dims, avq_dtype dtype, int backward);
 
 /*
  * avq_selftest_wait -- self-test of the failure path of the kernels' bounded
