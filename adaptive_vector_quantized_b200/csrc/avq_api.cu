@@ -181,6 +181,26 @@ cudaError_t make_tmap_3d_bf16(CUtensorMap* map, const void* base, int inner, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_view_bf16(CUtensorMap* map, const void* base, const Strides& s, int B, int H, int N, int d,
+                                int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const int64_t st[3] = {s.n, s.h, s.b};
+  const int n[3] = {N, H, B};
+  cuuint64_t dims[4] = {(cuuint64_t)d, 1, 1, 1};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] != 0) dims[i + 1] = (cuuint64_t)n[i];
+    strides[i] = (cuuint64_t)(st[i] != 0 ? st[i] : d) * 2;
+  }
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace avq
 
 using namespace avq;

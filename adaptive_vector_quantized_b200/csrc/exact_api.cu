@@ -33,8 +33,8 @@ avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, 
   const int64_t es = (int64_t)elem(dt);
   int64_t last = d;
   for (int i = 0; i < 3; ++i) {
-    if (v[i] < 0 || v[i] > (int64_t)1 << 40)
-      return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be in [0, 2^40]", name);
+    if (v[i] < 0 || v[i] >= (int64_t)1 << 38)  // bytes below 2^40, a tensor map's limit
+      return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be in [0, 2^38)", name);
     if (v[i] * es % 16 != 0)
       return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", name);
     if (output && n[i] > 1 && v[i] < d)
@@ -171,7 +171,8 @@ long long tiles64(long long n) { return (n + 63) / 64; }
 
 // How a call is carried out, from its sizes, type and path alone.
 struct CrossPlan {
-  int splits = 1;  // forward
+  bool tc = false;  // tensor-core kernels
+  int splits = 1;   // forward
   int dkv_splits = 1, dq_splits = 1;
   size_t part = 0, part_lse = 0, delta = 0;  // bytes, each a multiple of 256
   size_t total() const { return part + part_lse + delta; }
@@ -183,8 +184,13 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   const long long rows = (long long)s.B * s.Hq * s.Nq, keys = (long long)s.Bk * s.Hk * s.Nk;
   const long long row_items = (long long)s.B * s.Hq * tiles64(s.Nq), key_items = (long long)s.Bk * s.Hk * tiles64(s.Nk);
   const long long row_units = (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * tiles64(s.Nq);
+  p.tc = dt == AVQ_BF16 && api_path() != AVQ_PATH_SIMT && s.Nk > 0;
   if (!backward) {
     p.splits = split_count(row_items, tiles64(s.Nk), target);
+    if (p.tc) {  // one block per SM, pairs of 128-row tiles, 128-key tiles
+      const long long pairs = (long long)s.B * s.Hq * ((s.Nq + 255) / 256);
+      p.splits = split_count(pairs, (s.Nk + 127) / 128, num_sms());
+    }
     if (p.splits > 1) {
       p.part = up256((size_t)p.splits * rows * s.d * 4);
       p.part_lse = up256((size_t)p.splits * rows * 4);
@@ -350,7 +356,14 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log{};
-  cudaError_t e = launch_cross_simt(a, dtype, cs, log);
+  cudaError_t e;
+  if (p.tc) {
+    unsigned int* err = error_word();
+    if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");
+    e = launch_cross_tc(a, err, cs, log);
+  } else {
+    e = launch_cross_simt(a, dtype, cs, log);
+  }
   if (e == cudaSuccess && a.splits > 1) e = launch_cross_join(a, dtype, cs, log);
   return api_finish(e, "cross attention launch", log);
 }

@@ -22,6 +22,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The same, but NaN if any of the three is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 2^x for two values on the FMA pipe instead of the special-function unit.
 // Range reduction to the nearest integer (Cody and Waite): j = round(x) by
 // adding and subtracting 1.5 * 2^23 (exact round-to-nearest for |x| < 2^22),

@@ -165,6 +165,15 @@ avq_status api_finish(cudaError_t e, const char* where, const LaunchLog& log);
 int api_path();
 bool api_injected(const char* entry);
 
+// 4-D tiled TMA map over a bf16 view [B][H][N][d] with the given strides, box
+// {64, box_rows, 1, 1}, 128-byte swizzle, zero fill out of bounds.  A dimension
+// with stride 0 becomes one of size 1: its coordinate is then always 0.
+cudaError_t make_tmap_view_bf16(CUtensorMap* map, const void* base, const Strides& s, int B, int H, int N, int d,
+                                int box_rows);
+
+// Tensor-core kernels of the cross attention (bf16).
+cudaError_t launch_cross_tc(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
+
 // Device address of the current device's error word.
 unsigned int* error_word();
 // One thread waits, with the given limit, on an mbarrier that nothing
