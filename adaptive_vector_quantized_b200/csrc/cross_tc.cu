@@ -137,155 +137,155 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   auto tO = [&](int t) { return tmem + 2 * kKeyTile + t * D; };
 
   if (warp >= kSoftmaxWarps) {
-   tc::regs_give<kOtherRegs>();
-   if (warp == kLoadWarp) {
-    if (lane == 0) {
-      uint32_t n = 0, q = 0;  // K and V tiles, items' Q loaded so far
+    tc::regs_give<kOtherRegs>();
+    if (warp == kLoadWarp) {
+      if (lane == 0) {
+        uint32_t n = 0, q = 0;  // K and V tiles, items' Q loaded so far
+        bool ok = true;
+        for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+          const Item x = item_of(a, i, pairs);
+          if (x.t0 >= x.t1) continue;
+          const int buf = q % S::kQBufs;
+          ok = guard.wait(q_empty + buf, (q / S::kQBufs & 1) ^ 1);
+          if (!ok) break;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, const Strides& st, int row, int h, int b, uint64_t* bar) {
+            tc::mbar_arrive_expect_tx(bar, S::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < KB; ++c)
+              tc::tma_load_4d(dst + c * kKeyTile * 128, map, c * 64, row, st.h != 0 ? h : 0, st.b != 0 ? b : 0, bar);
+          };
+          auto load_kv = [&](int j, bool v) {
+            const int slot = n % S::kSlots;
+            if (!guard.wait(empty + slot, (n / S::kSlots & 1) ^ 1)) return false;
+            load(sm + S::kRing + slot * S::kTileBytes, v ? &maps.v : &maps.k, v ? a.vs : a.ks, j * kKeyTile, x.kh, x.kb,
+                 full + slot);
+            ++n;
+            return true;
+          };
+          uint8_t* dst = sm + S::kQ + buf * 2 * S::kTileBytes;
+          load(dst, &maps.q, a.qs, x.row0, x.h, x.b, q_full + 2 * buf);
+          ok = load_kv(x.t0, false);
+          if (x.tiles == 2)
+            load(dst + S::kTileBytes, &maps.q, a.qs, x.row0 + kRowTile, x.h, x.b, q_full + 2 * buf + 1);
+          else
+            tc::mbar_arrive(q_full + 2 * buf + 1);  // keeps the phases alike
+          ++q;
+          for (int j = x.t0; j < x.t1 && ok; ++j) {
+            ok = load_kv(j, true);
+            if (ok && j + 1 < x.t1) ok = load_kv(j + 1, false);
+          }
+        }
+        // nothing of this block's copies may be in flight when it ends
+        for (uint32_t k = n > S::kSlots ? n - S::kSlots : 0; k < n; ++k)
+          tc::mbar_wait(full + k % S::kSlots, k / S::kSlots & 1, 1000000ull);
+        for (uint32_t k = q > S::kQBufs ? q - S::kQBufs : 0; k < q; ++k)
+          for (int t = 0; t < 2; ++t)
+            tc::mbar_wait(q_full + 2 * (k % S::kQBufs) + t, k / S::kQBufs & 1, 1000000ull);
+      }
+    } else if (warp == kMmaWarp) {
+      // Steps: (item, key tile) in the order of the softmax groups.  Each turn of
+      // the loop issues P V of one step and, tile by tile behind it, S of the next.
+      struct Step {
+        int i, j, t0, t1, count, kb, tiles;
+      };
+      auto settle = [&](Step& s) {  // the first step at or after item s.i
+        for (; s.i < items; s.i += gridDim.x) {
+          const Item x = item_of(a, s.i, pairs);
+          s.j = s.t0 = x.t0;
+          s.t1 = x.t1;
+          s.count = x.count;
+          s.kb = x.kb;
+          s.tiles = x.tiles;
+          if (s.t0 < s.t1) return;
+        }
+        s.tiles = 0;
+      };
+      uint32_t n = 0, q = 0, p_phase = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
-        const Item x = item_of(a, i, pairs);
-        if (x.t0 >= x.t1) continue;
-        const int buf = q % S::kQBufs;
-        ok = guard.wait(q_empty + buf, (q / S::kQBufs & 1) ^ 1);
-        if (!ok) break;
-        auto load = [&](uint8_t* dst, const CUtensorMap* map, const Strides& st, int row, int h, int b, uint64_t* bar) {
-          tc::mbar_arrive_expect_tx(bar, S::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < KB; ++c)
-            tc::tma_load_4d(dst + c * kKeyTile * 128, map, c * 64, row, st.h != 0 ? h : 0, st.b != 0 ? b : 0, bar);
-        };
-        auto load_kv = [&](int j, bool v) {
-          const int slot = n % S::kSlots;
-          if (!guard.wait(empty + slot, (n / S::kSlots & 1) ^ 1)) return false;
-          load(sm + S::kRing + slot * S::kTileBytes, v ? &maps.v : &maps.k, v ? a.vs : a.ks, j * kKeyTile, x.kh, x.kb,
-               full + slot);
+      Step cur{}, next{};  // cur: no tiles yet
+      next.i = blockIdx.x;
+      settle(next);
+      const uint64_t ring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 16, 1024);
+      const uint64_t qtile = tc::sdesc_sw128(tc::smem_u32(sm + S::kQ), 16, 1024);
+      const uint64_t vring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), kKeyTile * 128, 1024);
+      int buf = 0;
+      while (ok && cur.tiles + next.tiles > 0) {
+        uint32_t vslot = 0;
+        if (cur.tiles > 0) {
+          vslot = n % S::kSlots;
+          ok = guard.wait(full + vslot, n / S::kSlots & 1);
+          if (!ok) break;
           ++n;
-          return true;
-        };
-        uint8_t* dst = sm + S::kQ + buf * 2 * S::kTileBytes;
-        load(dst, &maps.q, a.qs, x.row0, x.h, x.b, q_full + 2 * buf);
-        ok = load_kv(x.t0, false);
-        if (x.tiles == 2)
-          load(dst + S::kTileBytes, &maps.q, a.qs, x.row0 + kRowTile, x.h, x.b, q_full + 2 * buf + 1);
-        else
-          tc::mbar_arrive(q_full + 2 * buf + 1);  // keeps the phases alike
-        ++q;
-        for (int j = x.t0; j < x.t1 && ok; ++j) {
-          ok = load_kv(j, true);
-          if (ok && j + 1 < x.t1) ok = load_kv(j + 1, false);
+          const int k0 = cur.j * kKeyTile;
+          if (!tile_full(a, k0, cur.count))
+            clear_rows<D>(sm + S::kRing + vslot * S::kTileBytes, key_bits(a, cur.kb, k0, cur.count, lane),
+                          (cur.count - k0 + 15) & ~15, lane);
         }
-      }
-      // nothing of this block's copies may be in flight when it ends
-      for (uint32_t k = n > S::kSlots ? n - S::kSlots : 0; k < n; ++k)
-        tc::mbar_wait(full + k % S::kSlots, k / S::kSlots & 1, 1000000ull);
-      for (uint32_t k = q > S::kQBufs ? q - S::kQBufs : 0; k < q; ++k)
-        for (int t = 0; t < 2; ++t)
-          tc::mbar_wait(q_full + 2 * (k % S::kQBufs) + t, k / S::kQBufs & 1, 1000000ull);
-    }
-   } else if (warp == kMmaWarp) {
-    // Steps: (item, key tile) in the order of the softmax groups.  Each turn of
-    // the loop issues P V of one step and, tile by tile behind it, S of the next.
-    struct Step {
-      int i, j, t0, t1, count, kb, tiles;
-    };
-    auto settle = [&](Step& s) {  // the first step at or after item s.i
-      for (; s.i < items; s.i += gridDim.x) {
-        const Item x = item_of(a, s.i, pairs);
-        s.j = s.t0 = x.t0;
-        s.t1 = x.t1;
-        s.count = x.count;
-        s.kb = x.kb;
-        s.tiles = x.tiles;
-        if (s.t0 < s.t1) return;
-      }
-      s.tiles = 0;
-    };
-    uint32_t n = 0, q = 0, p_phase = 0;
-    bool ok = true;
-    Step cur{}, next{};  // cur: no tiles yet
-    next.i = blockIdx.x;
-    settle(next);
-    const uint64_t ring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 16, 1024);
-    const uint64_t qtile = tc::sdesc_sw128(tc::smem_u32(sm + S::kQ), 16, 1024);
-    const uint64_t vring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), kKeyTile * 128, 1024);
-    int buf = 0;
-    while (ok && cur.tiles + next.tiles > 0) {
-      uint32_t vslot = 0;
-      if (cur.tiles > 0) {
-        vslot = n % S::kSlots;
-        ok = guard.wait(full + vslot, n / S::kSlots & 1);
-        if (!ok) break;
-        ++n;
-        const int k0 = cur.j * kKeyTile;
-        if (!tile_full(a, k0, cur.count))
-          clear_rows<D>(sm + S::kRing + vslot * S::kTileBytes, key_bits(a, cur.kb, k0, cur.count, lane),
-                        (cur.count - k0 + 15) & ~15, lane);
-      }
-      const uint32_t kslot = n % S::kSlots;
-      const bool fresh = next.j == next.t0;  // the next step starts an item
-      if (next.tiles > 0 && fresh) buf = q % S::kQBufs;
+        const uint32_t kslot = n % S::kSlots;
+        const bool fresh = next.j == next.t0;  // the next step starts an item
+        if (next.tiles > 0 && fresh) buf = q % S::kQBufs;
 #pragma unroll 1
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (t < cur.tiles) {
-          ok = guard.wait(p_ready + t, p_phase >> t & 1);
-          if (!ok) break;
-          p_phase ^= 1u << t;
-          tc::tc_fence_after();
-          if (lane == 0) {
-            const uint32_t idesc = tc::idesc_bf16(kRowTile, D, 0, 1);
-            const int ksteps = min(kKeyTile, cur.count - cur.j * kKeyTile + 15) >> 4;
-            uint64_t vd = vring + (vslot * S::kTileBytes >> 4);
-            uint32_t pa = tS(t), more = cur.j > cur.t0;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (t < cur.tiles) {
+            ok = guard.wait(p_ready + t, p_phase >> t & 1);
+            if (!ok) break;
+            p_phase ^= 1u << t;
+            tc::tc_fence_after();
+            if (lane == 0) {
+              const uint32_t idesc = tc::idesc_bf16(kRowTile, D, 0, 1);
+              const int ksteps = min(kKeyTile, cur.count - cur.j * kKeyTile + 15) >> 4;
+              uint64_t vd = vring + (vslot * S::kTileBytes >> 4);
+              uint32_t pa = tS(t), more = cur.j > cur.t0;
 #pragma unroll 1
-            for (int k = 0; k < ksteps; ++k) {
-              tc::mma_bf16_ts(tO(t), pa, vd, idesc, more);
-              vd += 2048 >> 4;
-              pa += 8;
-              more = 1;
+              for (int k = 0; k < ksteps; ++k) {
+                tc::mma_bf16_ts(tO(t), pa, vd, idesc, more);
+                vd += 2048 >> 4;
+                pa += 8;
+                more = 1;
+              }
+              if (cur.j + 1 == cur.t1) tc::mma_commit(o_full + t);
             }
-            if (cur.j + 1 == cur.t1) tc::mma_commit(o_full + t);
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        if (t < next.tiles) {
-          if (t == 0) ok = guard.wait(full + kslot, n / S::kSlots & 1);
-          if (ok && fresh) ok = guard.wait(q_full + 2 * buf + t, q / S::kQBufs & 1);
-          if (!ok) break;
-          if (lane == 0) {
-            const int left = next.count - next.j * kKeyTile;
-            const uint32_t idesc = tc::idesc_bf16(kRowTile, left >= kKeyTile ? kKeyTile : (left + 15) & ~15, 0, 0);
-            const uint64_t qd = qtile + ((buf * 2 + t) * S::kTileBytes >> 4);
-            const uint64_t kd = ring + (kslot * S::kTileBytes >> 4);
+          if (t < next.tiles) {
+            if (t == 0) ok = guard.wait(full + kslot, n / S::kSlots & 1);
+            if (ok && fresh) ok = guard.wait(q_full + 2 * buf + t, q / S::kQBufs & 1);
+            if (!ok) break;
+            if (lane == 0) {
+              const int left = next.count - next.j * kKeyTile;
+              const uint32_t idesc = tc::idesc_bf16(kRowTile, left >= kKeyTile ? kKeyTile : (left + 15) & ~15, 0, 0);
+              const uint64_t qd = qtile + ((buf * 2 + t) * S::kTileBytes >> 4);
+              const uint64_t kd = ring + (kslot * S::kTileBytes >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int off = ((k >> 2) * (kRowTile * 128) + (k & 3) * 32) >> 4;
-              tc::mma_bf16(tS(t), qd + off, kd + off, idesc, k > 0);
+              for (int k = 0; k < D / 16; ++k) {
+                const int off = ((k >> 2) * (kRowTile * 128) + (k & 3) * 32) >> 4;
+                tc::mma_bf16(tS(t), qd + off, kd + off, idesc, k > 0);
+              }
+              tc::mma_commit(s_full + t);
             }
-            tc::mma_commit(s_full + t);
+            __syncwarp();
           }
-          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0 && cur.tiles > 0) tc::mma_commit(empty + vslot);
+        if (next.tiles > 0) {
+          if (lane == 0) tc::mma_commit(empty + kslot);
+          ++n;
+          if (fresh) ++q;
+          if (lane == 0 && next.j + 1 == next.t1) tc::mma_commit(q_empty + buf);
+        }
+        __syncwarp();
+        cur = next;
+        if (next.tiles > 0 && ++next.j == next.t1) {
+          next.i += gridDim.x;
+          settle(next);
         }
       }
-      if (!ok) break;
-      if (lane == 0 && cur.tiles > 0) tc::mma_commit(empty + vslot);
-      if (next.tiles > 0) {
-        if (lane == 0) tc::mma_commit(empty + kslot);
-        ++n;
-        if (fresh) ++q;
-        if (lane == 0 && next.j + 1 == next.t1) tc::mma_commit(q_empty + buf);
-      }
+      // every MMA done before TMEM is given back
+      if (lane == 0) tc::mma_commit(drain);
       __syncwarp();
-      cur = next;
-      if (next.tiles > 0 && ++next.j == next.t1) {
-        next.i += gridDim.x;
-        settle(next);
-      }
+      tc::mbar_wait(drain, 0, 1000000ull);
     }
-    // every MMA done before TMEM is given back
-    if (lane == 0) tc::mma_commit(drain);
-    __syncwarp();
-    tc::mbar_wait(drain, 0, 1000000ull);
-   }
   } else {
     tc::regs_take<kSoftmaxRegs>();
     const int t = warp >> 2;  // the group's tile of the pair

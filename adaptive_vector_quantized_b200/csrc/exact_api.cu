@@ -169,9 +169,13 @@ int split_count(long long items, long long units, long long target) {
 }
 long long tiles64(long long n) { return (n + 63) / 64; }
 
+// Rows per key head up to which the keys are streamed through registers.
+constexpr long long kFewRows = 32;
+
 // How a call is carried out, from its sizes, type and path alone.
 struct CrossPlan {
-  bool tc = false;  // tensor-core kernels
+  bool tc = false;   // tensor-core kernels
+  bool few = false;  // the one for few rows per key head
   int splits = 1;   // forward
   int dkv_splits = 1, dq_splits = 1;
   size_t part = 0, part_lse = 0, delta = 0;  // bytes, each a multiple of 256
@@ -187,7 +191,14 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   p.tc = dt == AVQ_BF16 && api_path() != AVQ_PATH_SIMT && s.Nk > 0;
   if (!backward) {
     p.splits = split_count(row_items, tiles64(s.Nk), target);
-    if (p.tc) {  // one block per SM, pairs of 128-row tiles, 128-key tiles
+    const long long shared = (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * s.Nq;  // rows that read one key head
+    p.few = p.tc && shared <= kFewRows;
+    if (p.few) {
+      // two rounds of the resident blocks, since lengths differ: 32 sequences
+      // of 4096 to 8191 keys took 68 us with 1 or 2 rounds, 71 with 4, 78 with 8
+      const long long blocks = (long long)s.Bk * s.Hk * ((shared + 15) / 16);
+      p.splits = split_count(blocks, s.Nk / 128, 4ll * num_sms());
+    } else if (p.tc) {  // one block per SM, pairs of 128-row tiles, 128-key tiles
       const long long pairs = (long long)s.B * s.Hq * ((s.Nq + 255) / 256);
       p.splits = split_count(pairs, (s.Nk + 127) / 128, num_sms());
     }
@@ -360,7 +371,7 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   if (p.tc) {
     unsigned int* err = error_word();
     if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");
-    e = launch_cross_tc(a, err, cs, log);
+    e = p.few ? launch_cross_few(a, err, cs, log) : launch_cross_tc(a, err, cs, log);
   } else {
     e = launch_cross_simt(a, dtype, cs, log);
   }
