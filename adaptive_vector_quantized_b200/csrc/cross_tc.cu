@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           const int k0 = cur.j * kKeyTile;
           if (!tile_full(a, k0, cur.count))
             clear_rows<D>(sm + S::kRing + vslot * S::kTileBytes, key_bits(a, cur.kb, k0, cur.count, lane),
-                          (cur.count - k0 + 15) & ~15, lane);
+                          min((cur.count - k0 + 15) & ~15, a.Nk - k0), lane);
         }
         const uint32_t kslot = n % S::kSlots;
         const bool fresh = next.j == next.t0;  // the next step starts an item

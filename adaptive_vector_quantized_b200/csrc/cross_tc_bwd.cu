@@ -1,0 +1,761 @@
+// Gradients of the exact attention on the tensor cores (bf16), without atomics:
+// dK and dV by blocks that own a tile of keys and walk the rows, dQ by blocks
+// that own a tile of rows and walk the keys.  S and dP are formed in both (7
+// products of tiles instead of 5), so that every sum has one owner and a fixed
+// order and no gradient passes through memory in fp32.
+//
+//   P = exp(S - lse),  dP = dO V^T,  dS = P (dP - delta),
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
+//
+// A block has two groups of four warps for the elementwise work (a TMEM lane to
+// a thread, half of the tile's columns to a group), a warp that issues MMAs, one
+// that loads by TMA and one that fetches lse and delta.  P and dS overwrite S
+// and dP in TMEM as bf16 and are first operands from there.  Elementwise work
+// and MMAs alternate in two phases that overlap:
+//   dK/dV:  P(j) | dK(j-1), dP(j)      dS(j) | dV(j), S(j+1)
+//   dQ:     P(j) | dQ(j-1), dP(j)      dS(j) | S(j+1)
+#include "cross_tc.cuh"
+
+namespace avq {
+
+namespace {
+
+constexpr int kWorkWarps = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kRowWarp = 10;
+constexpr int kThreads = 384;
+// registers: 168 a thread at launch, then 2 * 216 + 72 = 3 * 168
+constexpr int kWorkRegs = 216, kOtherRegs = 72;
+
+template <int D>
+struct Smem {
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kSlots = 4;                          // ring of the walked tiles
+  static constexpr int kOwn = 0;                            // the block's own two tiles; results staged there
+  static constexpr int kRing = 2 * kTileBytes;
+  static constexpr int kRows = kRing + kSlots * kTileBytes; // [2 stages][lse, delta][128]
+  static constexpr int kBar = kRows + 2 * 1024;
+  // full[slots], empty[slots], own_full, own_empty, s_full[2], dp_full, p_ready, ds_ready, done, rows_full[2],
+  // rows_empty[2], drain
+  static constexpr int kBars = 2 * kSlots + 13;
+  static constexpr int kMisc = kBar + kBars * 8;
+  static constexpr int kTotal = kMisc + 16;
+};
+
+struct Bars {
+  uint64_t *full, *empty, *own_full, *own_empty, *s_full, *dp_full, *p_ready, *ds_ready, *done, *rows_full,
+      *rows_empty, *drain;
+};
+template <int D>
+__device__ __forceinline__ Bars bars_of(uint8_t* sm) {
+  Bars b;
+  b.full = reinterpret_cast<uint64_t*>(sm + Smem<D>::kBar);
+  b.empty = b.full + Smem<D>::kSlots;
+  b.own_full = b.empty + Smem<D>::kSlots;
+  b.own_empty = b.own_full + 1;
+  b.s_full = b.own_empty + 1;
+  b.dp_full = b.s_full + 2;
+  b.p_ready = b.dp_full + 1;
+  b.ds_ready = b.p_ready + 1;
+  b.done = b.ds_ready + 1;
+  b.rows_full = b.done + 1;
+  b.rows_empty = b.rows_full + 2;
+  b.drain = b.rows_empty + 2;
+  return b;
+}
+template <int D>
+__device__ __forceinline__ void init_bars(const Bars& b) {
+  for (int i = 0; i < Smem<D>::kBars; ++i) {
+    uint64_t* x = b.full + i;
+    const bool all = x == b.own_empty || x == b.p_ready || x == b.ds_ready || x == b.rows_empty || x == b.rows_empty + 1;
+    tc::mbar_init(x, all ? kWorkWarps : 1);
+  }
+  tc::fence_mbar_init();
+}
+
+struct Maps {
+  CUtensorMap q, g, k, v, out0, out1;  // out: dV, dK, or dQ
+};
+
+// A [128 rows][D] tile by TMA
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, const Strides& st, int row, int h,
+                                          int b, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    tc::tma_load_4d(dst + c * 128 * 128, map, c * 64, row, st.h != 0 ? h : 0, st.b != 0 ? b : 0, bar);
+}
+
+// D[128 x 128] = A[128][D] B[128][D]^T, both tiles of rows in shared memory
+template <int D>
+__device__ __forceinline__ void mma_rows_rows(uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, 128, 0, 0);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const int off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+    tc::mma_bf16(d, a + off, b + off, idesc, k > 0);
+  }
+}
+// D[128 x D] (+)= A[128][16 steps] B[16 steps][D]: A in TMEM (two halves of 4
+// steps, 64 columns apart), B a tile of rows in shared memory
+template <int D>
+__device__ __forceinline__ void mma_tmem_cols(uint32_t d, uint32_t a, uint64_t b, int steps, uint32_t more) {
+  constexpr uint32_t idesc = tc::idesc_bf16(128, D, 0, 1);
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    tc::mma_bf16_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, b + k * (2048 >> 4), idesc, more);
+    more = 1;
+  }
+}
+
+// p = exp2(c2 s + nl) for 32 scores; packed to bf16 in out
+template <bool kVec>
+__device__ __forceinline__ void exp_chunk(const uint32_t* r, float2 c2, const float* nl, float2 nl1, float2* p) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 l = kVec ? fm::f2(nl[2 * i], nl[2 * i + 1]) : nl1;
+    const float2 x = fm::fma2(fm::f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, l);
+    p[i] = (i & 3) == 3 ? fm::exp2_poly2(x) : fm::f2(tc::ex2(x.x), tc::ex2(x.y));
+  }
+}
+
+// 64 columns of an accumulator row (times f), as bf16 into the warp's staging
+// rows, then to memory by TMA.
+__device__ __forceinline__ void store_block(uint32_t taddr, float f, uint8_t* out, const CUtensorMap* map, int col,
+                                            int row, int rows, int h, int b, int lane) {
+  if (lane == 0) tc::bulk_wait_group_read0();
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t o[32];
+    tc::tmem_ld32(taddr + c * 32, o);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint4 v;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16x2(__uint_as_float(o[k * 8 + 2 * e]) * f, __uint_as_float(o[k * 8 + 2 * e + 1]) * f);
+      *reinterpret_cast<uint4*>(out + lane * 128 + (((c * 4 + k) ^ (lane & 7)) << 4)) = v;
+    }
+  }
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (row < rows) tc::tma_store_4d(map, out, col, row, h, b);
+    tc::bulk_commit_group();
+  }
+}
+// The same row in fp32, straight to memory (partial results).
+template <int D>
+__device__ __forceinline__ void store_partial(uint32_t taddr, float f, float* dst, bool live) {
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tc::tmem_ld16(taddr + c * 16, o);
+    tc::tmem_wait_ld();
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < 16; k += 4)
+        *reinterpret_cast<float4*>(dst + c * 16 + k) =
+            make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f, __uint_as_float(o[k + 2]) * f,
+                        __uint_as_float(o[k + 3]) * f);
+    }
+  }
+}
+
+// ---- dK and dV -------------------------------------------------------------------
+
+struct KeyItem {
+  int kb, kh, k0, count, split;
+  long long i0, i1;  // row tiles of the query heads and entries that share the key head
+};
+__device__ __forceinline__ KeyItem key_item(const CrossArgs& a, int i, int ktiles, int rtiles) {
+  KeyItem x;
+  x.k0 = i % ktiles * 128;
+  const int rest = i / ktiles;
+  x.split = rest % a.splits;
+  const int bh = rest / a.splits;
+  x.kb = bh / a.Hk;
+  x.kh = bh % a.Hk;
+  x.count = key_count(a, x.kb);
+  const long long all = x.k0 < x.count ? (long long)(a.B / a.Bk) * (a.Hq / a.Hk) * rtiles : 0;
+  x.i0 = all * x.split / a.splits;
+  x.i1 = all * (x.split + 1) / a.splits;
+  return x;
+}
+struct RowTile {
+  int b, h, row0;
+};
+__device__ __forceinline__ RowTile row_tile(const CrossArgs& a, const KeyItem& x, long long i, int rtiles) {
+  const int R = a.B / a.Bk, G = a.Hq / a.Hk;
+  const int rg = (int)(i / rtiles);
+  return RowTile{x.kb * R + rg / G, x.kh * G + rg % G, (int)(i % rtiles) * 128};
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_constant__ Maps maps,
+                                                                  const CrossArgs a, unsigned int* err, int items,
+                                                                  int ktiles, int rtiles) {
+  using S = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Bars bar = bars_of<D>(sm);
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
+  int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
+  float* sRows = reinterpret_cast<float*>(sm + S::kRows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    init_bars<D>(bar);
+    *sAbort = 0;
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(sTmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const Guard guard{err, sAbort};
+  const uint32_t tmem = *sTmem;
+  const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 256 + D;  // S | dP | dV | dK
+
+  if (warp >= kWorkWarps) {
+    tc::regs_give<kOtherRegs>();
+    if (warp == kLoadWarp) {
+      if (lane == 0) {
+        uint32_t n = 0, own = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+          const KeyItem x = key_item(a, i, ktiles, rtiles);
+          if (x.i0 >= x.i1) continue;
+          ok = guard.wait(bar.own_empty, (own & 1) ^ 1);
+          if (!ok) break;
+          tc::mbar_arrive_expect_tx(bar.own_full, 2 * S::kTileBytes);
+          load_tile<D>(sm + S::kOwn, &maps.k, a.ks, x.k0, x.kh, x.kb, bar.own_full);
+          load_tile<D>(sm + S::kOwn + S::kTileBytes, &maps.v, a.vs, x.k0, x.kh, x.kb, bar.own_full);
+          ++own;
+          for (long long j = 2 * x.i0; j < 2 * x.i1; ++j, ++n) {  // Q, then dO of each row tile
+            const RowTile r = row_tile(a, x, j >> 1, rtiles);
+            const int slot = n % S::kSlots;
+            ok = guard.wait(bar.empty + slot, (n / S::kSlots & 1) ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(bar.full + slot, S::kTileBytes);
+            const bool g = j & 1;
+            load_tile<D>(sm + S::kRing + slot * S::kTileBytes, g ? &maps.g : &maps.q, g ? a.gs : a.qs, r.row0, r.h,
+                         r.b, bar.full + slot);
+          }
+        }
+        for (uint32_t k = n > S::kSlots ? n - S::kSlots : 0; k < n; ++k)
+          tc::mbar_wait(bar.full + k % S::kSlots, k / S::kSlots & 1, 1000000ull);
+        if (own > 0) tc::mbar_wait(bar.own_full, (own - 1) & 1, 1000000ull);
+      }
+    } else if (warp == kRowWarp) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        const KeyItem x = key_item(a, i, ktiles, rtiles);
+        for (long long j = x.i0; j < x.i1; ++j, ++n) {
+          const RowTile r = row_tile(a, x, j, rtiles);
+          const size_t head = ((size_t)r.b * a.Hq + r.h) * a.Nq;
+          float l[4], d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = r.row0 + 32 * e + lane;
+            const bool in = row < a.Nq;  // past the end: P = exp2(-inf)
+            l[e] = in ? -__ldg(a.lse + head + row) * kLog2e : -INFINITY;
+            d[e] = in ? -__ldg(a.delta + head + row) : 0.f;
+          }
+          ok = guard.wait(bar.rows_empty + (n & 1), (n >> 1 & 1) ^ 1);
+          if (!ok) break;
+          float* dst = sRows + (n & 1) * 256;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dst[32 * e + lane] = l[e];
+            dst[128 + 32 * e + lane] = d[e];
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar.rows_full + (n & 1));
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
+      const uint64_t ring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 16, 1024);
+      const uint64_t ring_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 128 * 128, 1024);
+      constexpr int kTile16 = S::kTileBytes >> 4;
+      uint32_t n = 0, own_n = 0, steps = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        const KeyItem x = key_item(a, i, ktiles, rtiles);
+        if (x.i0 >= x.i1) continue;
+        ok = guard.wait(bar.own_full, own_n & 1) && guard.wait(bar.full + n % S::kSlots, n / S::kSlots & 1);
+        if (!ok) break;
+        ++own_n;
+        if (lane == 0) {
+          mma_rows_rows<D>(tS, own, ring + n % S::kSlots * kTile16);  // S^T = K Q^T
+          tc::mma_commit(bar.s_full);
+        }
+        __syncwarp();
+        ok = guard.wait(bar.full + (n + 1) % S::kSlots, (n + 1) / S::kSlots & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          mma_rows_rows<D>(tP, own + kTile16, ring + (n + 1) % S::kSlots * kTile16);  // dP^T = V dO^T
+          tc::mma_commit(bar.dp_full);
+        }
+        __syncwarp();
+        for (long long j = x.i0; j < x.i1; ++j, n += 2, ++steps) {
+          const uint32_t qs = n % S::kSlots, gs = (n + 1) % S::kSlots;
+          const bool last = j + 1 == x.i1;
+          ok = guard.wait(bar.p_ready, steps & 1) &&
+               (last || guard.wait(bar.full + (n + 2) % S::kSlots, (n + 2) / S::kSlots & 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lane == 0) {
+            mma_tmem_cols<D>(tV, tS, ring_mn + gs * kTile16, 8, j > x.i0);  // dV += P^T dO
+            tc::mma_commit(bar.empty + gs);
+            if (!last) {
+              mma_rows_rows<D>(tS, own, ring + (n + 2) % S::kSlots * kTile16);
+              tc::mma_commit(bar.s_full);
+            }
+          }
+          __syncwarp();
+          ok = guard.wait(bar.ds_ready, steps & 1) &&
+               (last || guard.wait(bar.full + (n + 3) % S::kSlots, (n + 3) / S::kSlots & 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lane == 0) {
+            mma_tmem_cols<D>(tK, tP, ring_mn + qs * kTile16, 8, j > x.i0);  // dK += dS^T Q
+            tc::mma_commit(bar.empty + qs);
+            if (!last) {
+              mma_rows_rows<D>(tP, own + kTile16, ring + (n + 3) % S::kSlots * kTile16);
+              tc::mma_commit(bar.dp_full);
+            } else {
+              tc::mma_commit(bar.done);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0) tc::mma_commit(bar.drain);
+      __syncwarp();
+      tc::mbar_wait(bar.drain, 0, 1000000ull);
+    }
+  } else {
+    tc::regs_take<kWorkRegs>();
+    const int half = warp >> 2, quarter = warp & 3;  // rows 64 half .. + 63 of the row tile; key lanes of the tile
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    uint8_t* out = sm + S::kOwn + warp * 4096;
+    const float c2f = a.scale * kLog2e;
+    const float2 c2 = fm::f2(c2f, c2f);
+    uint32_t steps = 0, dones = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      const KeyItem x = key_item(a, i, ktiles, rtiles);
+      const int key = x.k0 + quarter * 32 + lane;
+      const bool live = key_seen(a, x.kb, key, x.count);
+      for (long long j = x.i0; j < x.i1; ++j, ++steps) {
+        const float* rows = sRows + (steps & 1) * 256 + half * 64;
+        ok = guard.wait(bar.rows_full + (steps & 1), steps >> 1 & 1) && guard.wait(bar.s_full, steps & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float2 p[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32], w[16];
+          float nl[32];
+          tc::tmem_ld32(tS + lane_off + half * 64 + c * 32, r);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(nl + e) = *reinterpret_cast<const float4*>(rows + c * 32 + e);
+          tc::tmem_wait_ld();
+          exp_chunk<true>(r, c2, nl, c2, p + c * 16);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (!live) p[c * 16 + e] = fm::f2(0.f, 0.f);  // whatever stands in the key's row
+            w[e] = pack_bf16x2(p[c * 16 + e].x, p[c * 16 + e].y);
+          }
+          tc::tmem_st16(tS + lane_off + half * 64 + c * 16, w);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar.p_ready);
+        ok = guard.wait(bar.dp_full, steps & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32], w[16];
+          float nd[32];
+          tc::tmem_ld32(tP + lane_off + half * 64 + c * 32, r);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(nd + e) = *reinterpret_cast<const float4*>(rows + 128 + c * 32 + e);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 d = fm::add2(fm::f2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])),
+                                fm::f2(nd[2 * e], nd[2 * e + 1]));
+            d = fm::mul2(d, p[c * 16 + e]);
+            w[e] = live ? pack_bf16x2(d.x, d.y) : 0u;
+          }
+          tc::tmem_st16(tP + lane_off + half * 64 + c * 16, w);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(bar.ds_ready);
+          tc::mbar_arrive(bar.rows_empty + (steps & 1));
+        }
+      }
+      if (!ok) break;
+      // group 0 writes dV, group 1 dK
+      const bool any = x.i0 < x.i1;
+      const uint32_t acc = (half == 0 ? tV : tK) + lane_off;
+      const float f = half == 0 ? 1.f : a.scale;
+      const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
+      const size_t at = (((size_t)x.kb * a.Hk + x.kh) * a.Nk + key) * D;
+      if (any) {
+        ok = guard.wait(bar.done, dones & 1);
+        if (!ok) break;
+        ++dones;
+        tc::tc_fence_after();
+      }
+      if (a.splits > 1) {
+        float* dst = a.part + ((size_t)x.split * 2 + (half == 0 ? 1 : 0)) * elems + at;
+        if (any) {
+          store_partial<D>(acc, f, dst, key < a.Nk);
+        } else if (key < a.Nk) {
+          for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      } else if (any) {
+#pragma unroll
+        for (int cb = 0; cb < S::kBlocks; ++cb)
+          store_block(acc + cb * 64, f, out, half == 0 ? &maps.out0 : &maps.out1, cb * 64, x.k0 + quarter * 32, a.Nk,
+                      a.Hk > 1 ? x.kh : 0, a.Bk > 1 ? x.kb : 0, lane);
+      } else if (key < a.Nk) {
+        bf16* dst = static_cast<bf16*>(half == 0 ? a.dV : a.dK) + at;
+        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+      }
+      tc::tc_fence_before();
+      if (any) {
+        if (lane == 0) {
+          tc::bulk_wait_group_read0();  // K and V may be loaded over the staging rows
+          tc::mbar_arrive(bar.own_empty);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) tc::bulk_wait_group0();
+  }
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---- dQ ------------------------------------------------------------------------------
+
+struct RowItem {
+  int b, h, kb, kh, row0, count, t0, t1, split;
+};
+__device__ __forceinline__ RowItem row_item(const CrossArgs& a, int i, int rtiles) {
+  RowItem x;
+  x.row0 = i % rtiles * 128;
+  const int rest = i / rtiles;
+  x.split = rest % a.splits;
+  const int bh = rest / a.splits;
+  x.b = bh / a.Hq;
+  x.h = bh % a.Hq;
+  x.kb = x.b / (a.B / a.Bk);
+  x.kh = x.h / (a.Hq / a.Hk);
+  x.count = key_count(a, x.kb);
+  const int kt = (x.count + 127) / 128;
+  x.t0 = (int)((long long)kt * x.split / a.splits);
+  x.t1 = (int)((long long)kt * (x.split + 1) / a.splits);
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_constant__ Maps maps,
+                                                                 const CrossArgs a, unsigned int* err, int items,
+                                                                 int rtiles) {
+  using S = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Bars bar = bars_of<D>(sm);
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
+  int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    init_bars<D>(bar);
+    *sAbort = 0;
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(sTmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const Guard guard{err, sAbort};
+  const uint32_t tmem = *sTmem;
+  const uint32_t tP = tmem + 256, tQ = tmem + 384;  // S of even steps | S of odd steps | dP | dQ
+
+  if (warp >= kWorkWarps) {
+    tc::regs_give<kOtherRegs>();
+    if (warp == kLoadWarp) {
+      if (lane == 0) {
+        uint32_t n = 0, own = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+          const RowItem x = row_item(a, i, rtiles);
+          if (x.t0 >= x.t1) continue;
+          ok = guard.wait(bar.own_empty, (own & 1) ^ 1);
+          if (!ok) break;
+          tc::mbar_arrive_expect_tx(bar.own_full, 2 * S::kTileBytes);
+          load_tile<D>(sm + S::kOwn, &maps.q, a.qs, x.row0, x.h, x.b, bar.own_full);
+          load_tile<D>(sm + S::kOwn + S::kTileBytes, &maps.g, a.gs, x.row0, x.h, x.b, bar.own_full);
+          ++own;
+          for (int j = 2 * x.t0; j < 2 * x.t1; ++j, ++n) {  // K, then V of each tile
+            const int slot = n % S::kSlots;
+            ok = guard.wait(bar.empty + slot, (n / S::kSlots & 1) ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(bar.full + slot, S::kTileBytes);
+            const bool v = j & 1;
+            load_tile<D>(sm + S::kRing + slot * S::kTileBytes, v ? &maps.v : &maps.k, v ? a.vs : a.ks, (j >> 1) * 128,
+                         x.kh, x.kb, bar.full + slot);
+          }
+        }
+        for (uint32_t k = n > S::kSlots ? n - S::kSlots : 0; k < n; ++k)
+          tc::mbar_wait(bar.full + k % S::kSlots, k / S::kSlots & 1, 1000000ull);
+        if (own > 0) tc::mbar_wait(bar.own_full, (own - 1) & 1, 1000000ull);
+      }
+    } else if (warp == kMmaWarp) {
+      const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
+      const uint64_t ring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 16, 1024);
+      const uint64_t ring_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 128 * 128, 1024);
+      constexpr int kTile16 = S::kTileBytes >> 4;
+      uint32_t n = 0, own_n = 0, steps = 0;
+      bool ok = true;
+      // S of the step whose K is the n-th tile of the ring: Q K^T, the keys that
+      // are left out cleared first, since K is a factor of dS K too
+      auto score = [&](const RowItem& x, int j, uint32_t at, uint32_t step) {
+        const uint32_t slot = at % S::kSlots;
+        if (!guard.wait(bar.full + slot, at / S::kSlots & 1)) return false;
+        if (!tile_full(a, j * 128, x.count))  // rows past the tensor's end came as zeros
+          clear_rows<D>(sm + S::kRing + slot * S::kTileBytes, key_bits(a, x.kb, j * 128, x.count, lane),
+                        min(128, a.Nk - j * 128), lane);
+        if (lane == 0) {
+          mma_rows_rows<D>(tmem + (step & 1) * 128, own, ring + slot * kTile16);
+          tc::mma_commit(bar.s_full + (step & 1));
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        const RowItem x = row_item(a, i, rtiles);
+        if (x.t0 >= x.t1) continue;
+        ok = guard.wait(bar.own_full, own_n & 1) && score(x, x.t0, n, steps) &&
+             guard.wait(bar.full + (n + 1) % S::kSlots, (n + 1) / S::kSlots & 1);
+        if (!ok) break;
+        ++own_n;
+        if (lane == 0) {
+          mma_rows_rows<D>(tP, own + kTile16, ring + (n + 1) % S::kSlots * kTile16);  // dP = dO V^T
+          tc::mma_commit(bar.dp_full);
+          tc::mma_commit(bar.empty + (n + 1) % S::kSlots);
+        }
+        __syncwarp();
+        for (int j = x.t0; j < x.t1; ++j, n += 2, ++steps) {
+          const uint32_t ks = n % S::kSlots;
+          const bool last = j + 1 == x.t1;
+          // S of the next step into the other half, which dS of the step before
+          // this one was formed from
+          ok = (last || score(x, j + 1, n + 2, steps + 1)) && guard.wait(bar.ds_ready, steps & 1) &&
+               (last || guard.wait(bar.full + (n + 3) % S::kSlots, (n + 3) / S::kSlots & 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lane == 0) {
+            mma_tmem_cols<D>(tQ, tP, ring_mn + ks * kTile16, 8, j > x.t0);  // dQ += dS K
+            tc::mma_commit(bar.empty + ks);
+            if (!last) {
+              const uint32_t vs = (n + 3) % S::kSlots;
+              mma_rows_rows<D>(tP, own + kTile16, ring + vs * kTile16);
+              tc::mma_commit(bar.dp_full);
+              tc::mma_commit(bar.empty + vs);
+            } else {
+              tc::mma_commit(bar.done);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0) tc::mma_commit(bar.drain);
+      __syncwarp();
+      tc::mbar_wait(bar.drain, 0, 1000000ull);
+    }
+  } else {
+    tc::regs_take<kWorkRegs>();
+    const int half = warp >> 2, quarter = warp & 3;  // keys 64 half .. + 63 of the key tile; row lanes of the tile
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    uint8_t* out = sm + S::kOwn + warp * 4096;
+    const float c2f = a.scale * kLog2e;
+    const float2 c2 = fm::f2(c2f, c2f);
+    uint32_t steps = 0, dones = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      const RowItem x = row_item(a, i, rtiles);
+      const int row = x.row0 + quarter * 32 + lane;
+      const size_t at = ((size_t)x.b * a.Hq + x.h) * a.Nq + row;
+      const bool in = row < a.Nq;
+      const float l = in ? -__ldg(a.lse + at) * kLog2e : -INFINITY;
+      const float dl = in ? -__ldg(a.delta + at) : 0.f;
+      const float2 nl = fm::f2(l, l), nd = fm::f2(dl, dl);
+      for (int j = x.t0; j < x.t1; ++j, ++steps) {
+        const bool whole = tile_full(a, j * 128, x.count);
+        uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
+        if (!whole) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            bits[w] = __ballot_sync(0xffffffffu, key_seen(a, x.kb, j * 128 + half * 64 + 32 * w + lane, x.count));
+        }
+        ok = guard.wait(bar.s_full + (steps & 1), steps >> 1 & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float2 p[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tc::tmem_ld32(tmem + (steps & 1) * 128 + lane_off + half * 64 + c * 32, r);
+          tc::tmem_wait_ld();
+          exp_chunk<false>(r, c2, nullptr, nl, p + c * 16);
+        }
+        ok = guard.wait(bar.dp_full, steps & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32], w[16];
+          tc::tmem_ld32(tP + lane_off + half * 64 + c * 32, r);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 d = fm::add2(fm::f2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), nd);
+            d = fm::mul2(d, p[c * 16 + e]);
+            if (!whole) {  // P or dP of a key that is left out may be anything
+              if (!(bits[c] >> (2 * e) & 1u)) d.x = 0.f;
+              if (!(bits[c] >> (2 * e + 1) & 1u)) d.y = 0.f;
+            }
+            w[e] = pack_bf16x2(d.x, d.y);
+          }
+          tc::tmem_st16(tP + lane_off + half * 64 + c * 16, w);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar.ds_ready);
+      }
+      if (!ok) break;
+      const bool any = x.t0 < x.t1;
+      if (any) {
+        ok = guard.wait(bar.done, dones & 1);
+        if (!ok) break;
+        ++dones;
+        tc::tc_fence_after();
+      }
+      // 64 columns of dQ to a group
+      if (half < S::kBlocks) {
+        if (a.splits > 1) {
+          float* dst = a.part + ((size_t)x.split * a.B * a.Hq * a.Nq + at) * D + half * 64;
+          if (any) {
+            store_partial<64>(tQ + lane_off + half * 64, a.scale, dst, in);
+          } else if (in) {
+            for (int c = 0; c < 64; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        } else if (any) {
+          store_block(tQ + lane_off + half * 64, a.scale, out, &maps.out0, half * 64, x.row0 + quarter * 32, a.Nq,
+                      a.Hq > 1 ? x.h : 0, a.B > 1 ? x.b : 0, lane);
+        } else if (in) {
+          bf16* dst = static_cast<bf16*>(a.dQ) + at * D + half * 64;
+          for (int c = 0; c < 64; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc::tc_fence_before();
+      if (any) {
+        if (lane == 0) {
+          tc::bulk_wait_group_read0();  // Q and dO may be loaded over the staging rows
+          tc::mbar_arrive(bar.own_empty);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) tc::bulk_wait_group0();
+  }
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+Strides dense(int B, int H, int N, int d) {
+  return Strides{B > 1 ? (int64_t)H * N * d : 0, H > 1 ? (int64_t)N * d : 0, N > 1 ? (int64_t)d : 0};
+}
+
+template <int D>
+cudaError_t maps_of(const CrossArgs& a, Maps* m) {
+  cudaError_t e = make_tmap_view_bf16(&m->q, a.Q, a.qs, a.B, a.Hq, a.Nq, D, 128);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m->g, a.G, a.gs, a.B, a.Hq, a.Nq, D, 128);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m->k, a.K, a.ks, a.Bk, a.Hk, a.Nk, D, 128);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m->v, a.V, a.vs, a.Bk, a.Hk, a.Nk, D, 128);
+  return e;
+}
+
+template <int D>
+cudaError_t run_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
+  Maps m;
+  const Strides s = dense(a.Bk, a.Hk, a.Nk, D);
+  cudaError_t e = maps_of<D>(a, &m);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dV, s, a.Bk, a.Hk, a.Nk, D, 32);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, s, a.Bk, a.Hk, a.Nk, D, 32);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = Smem<D>::kTotal + 1024;
+  e = cudaFuncSetAttribute(cross_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
+  const long long items = (long long)a.Bk * a.Hk * ktiles * a.splits;
+  const int grid = (int)(items < num_sms() ? items : num_sms());
+  cross_tc_dkv_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, (int)items, ktiles, rtiles);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
+  Maps m;
+  cudaError_t e = maps_of<D>(a, &m);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
+  if (e != cudaSuccess) return e;
+  m.out1 = m.out0;
+  constexpr int smem = Smem<D>::kTotal + 1024;
+  e = cudaFuncSetAttribute(cross_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int rtiles = (a.Nq + 127) / 128;
+  const long long items = (long long)a.B * a.Hq * rtiles * a.splits;
+  const int grid = (int)(items < num_sms() ? items : num_sms());
+  cross_tc_dq_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, (int)items, rtiles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
+  log.add("cross_tc_dkv");
+  return a.d == 64 ? run_dkv<64>(a, err, st) : run_dkv<128>(a, err, st);
+}
+cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
+  log.add("cross_tc_dq");
+  return a.d == 64 ? run_dq<64>(a, err, st) : run_dq<128>(a, err, st);
+}
+
+}  // namespace avq

@@ -211,6 +211,11 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   p.delta = up256((size_t)rows * 4);
   p.dq_splits = split_count(row_items, tiles64(s.Nk), target);
   if (key_items > 0) p.dkv_splits = split_count(key_items, row_units, target);
+  if (p.tc) {  // one block per SM, tiles of 128
+    const long long q = (s.Nq + 127) / 128, k = (s.Nk + 127) / 128;
+    p.dq_splits = split_count((long long)s.B * s.Hq * q, k, num_sms());
+    p.dkv_splits = split_count((long long)s.Bk * s.Hk * k, (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * q, num_sms());
+  }
   // dK and dV, then dQ, one after the other in the same place
   const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * rows * s.d * 4 : 0;
   const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * keys * s.d * 4 : 0;
@@ -425,11 +430,13 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   a.part = static_cast<float*>(ws);
   a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  unsigned int* err = error_word();
+  if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");
   LaunchLog log{};
   cudaError_t e = launch_cross_delta(a, dtype, cs, log);
   if (e == cudaSuccess && s.Nk > 0) {
     a.splits = p.dkv_splits;
-    e = launch_cross_simt_dkv(a, dtype, cs, log);
+    e = p.tc ? launch_cross_tc_dkv(a, err, cs, log) : launch_cross_simt_dkv(a, dtype, cs, log);
     if (a.splits > 1) {
       if (e == cudaSuccess) e = launch_partial_sum(dtype, a.part, 2 * kn, a.splits, dK, kn, cs, log);
       if (e == cudaSuccess) e = launch_partial_sum(dtype, a.part + kn, 2 * kn, a.splits, dV, kn, cs, log);
@@ -437,7 +444,7 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   }
   if (e == cudaSuccess) {
     a.splits = p.dq_splits;
-    e = launch_cross_simt_dq(a, dtype, cs, log);
+    e = p.tc ? launch_cross_tc_dq(a, err, cs, log) : launch_cross_simt_dq(a, dtype, cs, log);
     if (e == cudaSuccess && a.splits > 1) e = launch_partial_sum(dtype, a.part, qn, a.splits, dQ, qn, cs, log);
   }
   return api_finish(e, "cross attention backward launch", log);

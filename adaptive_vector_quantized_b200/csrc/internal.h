@@ -174,6 +174,8 @@ cudaError_t make_tmap_view_bf16(CUtensorMap* map, const void* base, const Stride
 // Tensor-core kernels of the cross attention (bf16).
 cudaError_t launch_cross_few(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_tc(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
+cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
+cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
 
 // Device address of the current device's error word.
 unsigned int* error_word();
