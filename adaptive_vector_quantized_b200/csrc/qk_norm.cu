@@ -29,7 +29,10 @@ namespace avq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // heads of one token in flight per lane group
+// Heads of a token that a lane group has under way at a time: 64 bytes of each
+// lane's loads, requested while the heads before are worked on.
+template <typename T>
+constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
 
 struct Params {
   const void* x[2];  // queries, keys
@@ -56,6 +59,51 @@ __device__ __forceinline__ void store4<float>(float* p, const float* v) {
 template <>
 __device__ __forceinline__ void store4<bf16>(bf16* p, const float* v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// A lane's 8 elements of a head as they stand in memory, each group of 4 by itself.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* x, int ia, int ib) {
+    a = __ldg(reinterpret_cast<const float4*>(x + ia));
+    b = __ldg(reinterpret_cast<const float4*>(x + ib));
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Raw<bf16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const bf16* x, int ia, int ib) {
+    a = __ldg(reinterpret_cast<const uint2*>(x + ia));
+    b = __ldg(reinterpret_cast<const uint2*>(x + ib));
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(b.x), v[5] = bf16_hi(b.x), v[6] = bf16_lo(b.y), v[7] = bf16_hi(b.y);
+  }
+};
+
+// Weights and biases of queries and keys in shared memory as fp32 (1 and 0 where absent).
+template <typename T, int D>
+__device__ __forceinline__ void fill_weights(const Params& p, float* sw, float* sb) {
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    const int which = i / D, c = i % D;
+    const T* w = static_cast<const T*>(p.w[which]);
+    const T* b = static_cast<const T*>(p.b[which]);
+    sw[i] = w != nullptr ? static_cast<float>(w[c]) : 1.f;
+    sb[i] = b != nullptr ? static_cast<float>(b[c]) : 0.f;
+  }
+}
+__device__ __forceinline__ void get8(const float* s, int ia, int ib, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(s + ia), b = *reinterpret_cast<const float4*>(s + ib);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
 template <int L>
@@ -143,12 +191,11 @@ __device__ __forceinline__ float normalise(float* v, float eps) {
 }
 
 template <typename T, int D, int kNorm, bool kHalf>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const Params p) {
-  constexpr int L = D / 8, G = kThreads / L;
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_kernel(const Params p) {
+  constexpr int L = D / 8, G = kThreads / L, U = kBatch<T>;
   __shared__ __align__(16) float2 tab[G * D / 2];
+  __shared__ __align__(16) float sw[kNorm == AVQ_NORM_NONE ? 4 : 2 * D], sb[kNorm == AVQ_NORM_NONE ? 4 : 2 * D];
   const int first = blockIdx.x * p.tb;
-  fill_table(p, tab, first);
-  __syncthreads();
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int t = group & (p.tb - 1), slot = group / p.tb, slots = G / p.tb;
   const int tok = first + t;
@@ -156,56 +203,61 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const Params p) {
   const int b = in ? tok / p.N : 0, n = in ? tok % p.N : 0;
   int ia, ib;
   const bool turned = places<kHalf>(lane, p.rot, ia, ib);
+  // batches of U heads: the queries' first, then the keys' (the same number for every group)
+  const int per = slots * U;
+  const int qb = (p.H[0] + per - 1) / per, all = qb + (p.H[1] + per - 1) / per;
+  Raw<T> raw[2][U];
+  auto request = [&](int i, Raw<T>* r) {
+    const int which = i >= qb, h0 = (which ? i - qb : i) * per + slot;
+    const T* x = static_cast<const T*>(p.x[which]) + b * p.xs[which].b + n * p.xs[which].n;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = h0 + k * slots;
+      if (in && h < p.H[which]) r[k].load(x + h * p.xs[which].h, ia, ib);
+      else r[k].clear();
+    }
+  };
   float2 cs[4];
+  auto finish = [&](int i, const Raw<T>* r) {
+    const int which = i >= qb, h0 = (which ? i - qb : i) * per + slot;
+    const int H = p.H[which];
+    T* y = static_cast<T*>(p.y[which]) + ((long long)b * H * p.N + n) * D;
+    float w[8], bias[8];
+    if constexpr (kNorm != AVQ_NORM_NONE) {
+      get8(sw + which * D, ia, ib, w);
+      get8(sb + which * D, ia, ib, bias);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int h = h0 + k * slots;
+      float v[8];
+      r[k].get(v);
+      if constexpr (kNorm != AVQ_NORM_NONE) {
+        normalise<D, kNorm>(v, p.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * w[e] + bias[e];
+      }
+      if (turned) turn<kHalf>(v, cs);
+      if (in && h < H) {
+        store4(y + (long long)h * p.N * D + ia, v);
+        store4(y + (long long)h * p.N * D + ib, v + 4);
+      }
+    }
+  };
+  request(0, raw[0]);  // under way while the table is made
+  fill_table(p, tab, first);
+  if constexpr (kNorm != AVQ_NORM_NONE) fill_weights<T, D>(p, sw, sb);
+  __syncthreads();
   if (turned) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) cs[i] = tab[t * (p.rot >> 1) + 4 * lane + i];
   }
-  for (int which = 0; which < 2; ++which) {
-    const int H = p.H[which];
-    const Strides xs = p.xs[which];
-    const T* x = static_cast<const T*>(p.x[which]) + b * xs.b + n * xs.n;
-    T* y = static_cast<T*>(p.y[which]) + ((long long)b * H * p.N + n) * D;
-    float w[8], bias[8];
-    if constexpr (kNorm != AVQ_NORM_NONE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.f, bias[i] = 0.f;
-      if (H > 0 && p.w[which] != nullptr) {
-        loadE<4>(static_cast<const T*>(p.w[which]) + ia, w);
-        loadE<4>(static_cast<const T*>(p.w[which]) + ib, w + 4);
-      }
-      if (H > 0 && p.b[which] != nullptr) {
-        loadE<4>(static_cast<const T*>(p.b[which]) + ia, bias);
-        loadE<4>(static_cast<const T*>(p.b[which]) + ib, bias + 4);
-      }
-    }
-    for (int h0 = 0; h0 < H; h0 += slots * kUnroll) {  // the same trips for every group
-      float v[kUnroll][8];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int h = h0 + k * slots + slot;
-        if (in && h < H) {
-          loadE<4>(x + h * xs.h + ia, v[k]);
-          loadE<4>(x + h * xs.h + ib, v[k] + 4);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int h = h0 + k * slots + slot;
-        if constexpr (kNorm != AVQ_NORM_NONE) {
-          normalise<D, kNorm>(v[k], p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * w[i] + bias[i];
-        }
-        if (turned) turn<kHalf>(v[k], cs);
-        if (in && h < H) {
-          store4(y + (long long)h * p.N * D + ia, v[k]);
-          store4(y + (long long)h * p.N * D + ib, v[k] + 4);
-        }
-      }
+  for (int i = 0; i < all; i += 2) {
+    if (i + 1 < all) request(i + 1, raw[1]);
+    finish(i, raw[0]);
+    if (i + 1 < all) {
+      if (i + 2 < all) request(i + 2, raw[0]);
+      finish(i + 1, raw[1]);
     }
   }
 }
@@ -214,9 +266,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const Params p) {
 // its share of the weight gradients in registers, summed over its groups at
 // the end in a fixed order.
 template <typename T, int D, int kNorm, bool kHalf>
-__global__ void __launch_bounds__(kThreads) qk_norm_backward_kernel(const Params p, int tiles) {
-  constexpr int L = D / 8, G = kThreads / L;
-  __shared__ __align__(16) float2 tab[G * D / 2];
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Params p, int tiles) {
+  constexpr int L = D / 8, G = kThreads / L, U = kBatch<T> / 2;
+  __shared__ __align__(16) float2 tab[2][G * D / 2];
   __shared__ float sums[G][D];
   const int which = blockIdx.y;
   const int H = p.H[which];
@@ -232,65 +284,93 @@ __global__ void __launch_bounds__(kThreads) qk_norm_backward_kernel(const Params
     loadE<4>(static_cast<const T*>(p.w[which]) + ia, w);
     loadE<4>(static_cast<const T*>(p.w[which]) + ib, w + 4);
   }
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int first = tile * p.tb;
-    fill_table(p, tab, first);
-    __syncthreads();
-    const int tok = first + t;
+  // batches of U heads of a tile's tokens, tile after tile
+  const int per = slots * U, batches = (H + per - 1) / per;
+  Raw<T> rx[2][U], rg[2][U];
+  auto request = [&](int tile, int i, Raw<T>* x, Raw<T>* g) {
+    const int tok = tile * p.tb + t;
     const bool in = tok < p.tokens;
     const int b = in ? tok / p.N : 0, n = in ? tok % p.N : 0;
-    float2 cs[4];
-    if (turned) {
+    const T* px = static_cast<const T*>(p.x[which]) + b * xs.b + n * xs.n;
+    const T* pg = static_cast<const T*>(p.g[which]) + b * gs.b + n * gs.n;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cs[i] = tab[t * (p.rot >> 1) + 4 * lane + i];
+    for (int k = 0; k < U; ++k) {
+      const int h = i * per + k * slots + slot;
+      if (in && h < H) {
+        x[k].load(px + h * xs.h, ia, ib);
+        g[k].load(pg + h * gs.h, ia, ib);
+      } else {
+        x[k].clear();
+        g[k].clear();
+      }
     }
-    __syncthreads();  // the table is rewritten for the next tile
-    const T* x = static_cast<const T*>(p.x[which]) + b * xs.b + n * xs.n;
-    const T* g = static_cast<const T*>(p.g[which]) + b * gs.b + n * gs.n;
+  };
+  float2 cs[4];
+  auto finish = [&](int tile, int i, const Raw<T>* rx, const Raw<T>* rg) {
+    const int tok = tile * p.tb + t;
+    const bool in = tok < p.tokens;
+    const int b = in ? tok / p.N : 0, n = in ? tok % p.N : 0;
     T* y = static_cast<T*>(p.y[which]) + ((long long)b * H * p.N + n) * D;
-    constexpr int U = 2;
-    for (int h0 = 0; h0 < H; h0 += slots * U) {
-      float u[U][8], z[U][8];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int h = h0 + k * slots + slot;
-        if (in && h < H) {
-          loadE<4>(x + h * xs.h + ia, u[k]);
-          loadE<4>(x + h * xs.h + ib, u[k] + 4);
-          loadE<4>(g + h * gs.h + ia, z[k]);
-          loadE<4>(g + h * gs.h + ib, z[k] + 4);
-        } else {
+    for (int k = 0; k < U; ++k) {
+      const int h = i * per + k * slots + slot;
+      const bool live = in && h < H;
+      float u[8], z[8];
+      rx[k].get(u);
+      rg[k].get(z);
+      if (turned) turn<kHalf>(z, cs);
+      const float r = normalise<D, kNorm>(u, p.eps);
+      float gu = 0.f, gm = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) u[k][i] = 0.f, z[k][i] = 0.f;
+      for (int e = 0; e < 8; ++e) {
+        if (live) {  // an absent row's u is 0 / 0 when eps is 0
+          dw[e] += z[e] * u[e];
+          db[e] += z[e];
         }
+        z[e] *= w[e];
+        gu += z[e] * u[e];
+        gm += z[e];
       }
+      gu = group_sum<L>(gu) * (1.f / D);
+      gm = kNorm == AVQ_NORM_LAYER ? group_sum<L>(gm) * (1.f / D) : 0.f;
+      if (live) {
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int h = h0 + k * slots + slot;
-        const bool live = in && h < H;
-        if (turned) turn<kHalf>(z[k], cs);
-        const float r = normalise<D, kNorm>(u[k], p.eps);
-        float gu = 0.f, gm = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (live) {  // an absent row's u is 0 / 0 when eps is 0
-            dw[i] += z[k][i] * u[k][i];
-            db[i] += z[k][i];
-          }
-          z[k][i] *= w[i];
-          gu += z[k][i] * u[k][i];
-          gm += z[k][i];
-        }
-        gu = group_sum<L>(gu) * (1.f / D);
-        gm = kNorm == AVQ_NORM_LAYER ? group_sum<L>(gm) * (1.f / D) : 0.f;
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[k][i] = (z[k][i] - gm - u[k][i] * gu) * r;
-          store4(y + (long long)h * p.N * D + ia, z[k]);
-          store4(y + (long long)h * p.N * D + ib, z[k] + 4);
-        }
+        for (int e = 0; e < 8; ++e) z[e] = (z[e] - gm - u[e] * gu) * r;
+        store4(y + (long long)h * p.N * D + ia, z);
+        store4(y + (long long)h * p.N * D + ib, z + 4);
       }
     }
+  };
+  // the batch after (tile, i)
+  auto next = [&](int& tile, int& i) {
+    if (++i == batches) {
+      i = 0;
+      tile += gridDim.x;
+    }
+  };
+  int tile = blockIdx.x, i = 0, made = 0;
+  if (tile < tiles) request(tile, i, rx[0], rg[0]);
+  // one turn of the loop handles two batches, so that the buffers' places are known
+  auto turn_of = [&](int cur) {
+    int nt = tile, ni = i;
+    next(nt, ni);
+    if (nt < tiles) request(nt, ni, rx[cur ^ 1], rg[cur ^ 1]);
+    if (i == 0) {  // a new tile: its sines and cosines, in the table that no one reads any more
+      fill_table(p, tab[made & 1], tile * p.tb);
+      __syncthreads();
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[e] = tab[made & 1][t * (p.rot >> 1) + 4 * lane + e];
+      }
+      ++made;
+    }
+    finish(tile, i, rx[cur], rg[cur]);
+    tile = nt;
+    i = ni;
+  };
+  while (tile < tiles) {
+    turn_of(0);
+    if (tile < tiles) turn_of(1);
   }
   for (int kind = 0; kind < 2; ++kind) {
     __syncthreads();
