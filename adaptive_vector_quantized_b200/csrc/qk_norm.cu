@@ -12,17 +12,21 @@
 //   dx = (g - u mean(g u) [- mean(g) for LayerNorm]) / sqrt(...),
 // u recomputed from x, so the forward pass keeps nothing.
 //
-// Angles are products in 64 bits, reduced to a fraction of a turn before the
-// rounding to 32 bits: at position 10^6 a 32-bit angle would be off by 0.06.
+// Angles are formed in 64-bit fixed point: a frequency as a fraction of a turn
+// in units of 2^-64, times the position as integers, where whole turns drop
+// off by themselves; only the remaining fraction is rounded to 32 bits.  (At
+// position 10^6 a 32-bit product would be off by 0.06.)
 //
 // The kernels are bound by memory: each element is read once and written
 // once.  A head is spread over d / 8 lanes of 8 elements, as two groups of 4
 // that hold both elements of every pair in either layout, so the rotation
 // needs no exchange between lanes and the norm 3 or 4 butterfly shuffles.
-// Sine and cosine are computed once per token and block (a table in shared
-// memory) and kept in registers over the token's heads.
+// A lane works out the sine and cosine of its own four pairs once per token and
+// keeps them over the token's heads: no table, no barrier.
 #include "common.cuh"
+#include "fastmath.cuh"
 #include "internal.h"
+#include "tc_util.cuh"
 
 namespace avq {
 
@@ -30,9 +34,14 @@ namespace {
 
 constexpr int kThreads = 256;
 // Heads of a token that a lane group has under way at a time: 64 bytes of each
-// lane's loads, requested while the heads before are worked on.
+// lane's loads, in each of two batches.  They are copied asynchronously into
+// places of shared memory that belong to one thread each, so that they take no
+// registers and need no barrier.  Measured for RMS norm with rotation of 65536
+// tokens of 32 heads of 64 (537 MB): 107 us with the batches in registers, where
+// the loads' latency bound it, 88 us like this (6.1 TB/s).
 template <typename T>
 constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+constexpr int kStages = 2;
 
 struct Params {
   const void* x[2];  // queries, keys
@@ -50,15 +59,11 @@ struct Params {
   float eps, mscale, sign;
 };
 
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float* v);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void store4(float* p, const float2* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
-template <>
-__device__ __forceinline__ void store4<bf16>(bf16* p, const float* v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+__device__ __forceinline__ void store4(bf16* p, const float2* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
 }
 
 // A lane's 8 elements of a head as they stand in memory, each group of 4 by itself.
@@ -66,27 +71,36 @@ template <typename T>
 struct Raw;
 template <>
 struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* x, int ia, int ib) {
-    a = __ldg(reinterpret_cast<const float4*>(x + ia));
-    b = __ldg(reinterpret_cast<const float4*>(x + ib));
-  }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  typedef float4 Four;
+  static __device__ __forceinline__ void get(float4 a, float4 b, float2* v) {
+    v[0] = fm::f2(a.x, a.y), v[1] = fm::f2(a.z, a.w), v[2] = fm::f2(b.x, b.y), v[3] = fm::f2(b.z, b.w);
   }
 };
 template <>
 struct Raw<bf16> {
-  uint2 a, b;
-  __device__ __forceinline__ void load(const bf16* x, int ia, int ib) {
-    a = __ldg(reinterpret_cast<const uint2*>(x + ia));
-    b = __ldg(reinterpret_cast<const uint2*>(x + ib));
+  typedef uint2 Four;
+  static __device__ __forceinline__ void get(uint2 a, uint2 b, float2* v) {
+    v[0] = fm::f2(bf16_lo(a.x), bf16_hi(a.x)), v[1] = fm::f2(bf16_lo(a.y), bf16_hi(a.y));
+    v[2] = fm::f2(bf16_lo(b.x), bf16_hi(b.x)), v[3] = fm::f2(bf16_lo(b.y), bf16_hi(b.y));
   }
-  __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(b.x), v[5] = bf16_hi(b.x), v[6] = bf16_lo(b.y), v[7] = bf16_hi(b.y);
+};
+// This thread's places for heads under way: [place][group][thread].
+template <typename T>
+struct Places {
+  typedef typename Raw<T>::Four Four;
+  Four* s;  // the thread's first
+  uint32_t addr;
+  __device__ __forceinline__ explicit Places(Four* ring) : s(ring + threadIdx.x), addr(tc::smem_u32(s)) {}
+  // x: the lane's first group, the second `apart` elements on
+  __device__ __forceinline__ void request(int k, const T* x, int apart) const {
+    copy(addr + (2 * k) * kThreads * (int)sizeof(Four), x);
+    copy(addr + (2 * k + 1) * kThreads * (int)sizeof(Four), x + apart);
+  }
+  __device__ __forceinline__ void get(int k, float2* v) const {
+    Raw<T>::get(s[(2 * k) * kThreads], s[(2 * k + 1) * kThreads], v);
+  }
+  static __device__ __forceinline__ void copy(uint32_t dst, const T* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"((int)sizeof(Four)) : "memory");
   }
 };
 
@@ -101,9 +115,9 @@ __device__ __forceinline__ void fill_weights(const Params& p, float* sw, float* 
     sb[i] = b != nullptr ? static_cast<float>(b[c]) : 0.f;
   }
 }
-__device__ __forceinline__ void get8(const float* s, int ia, int ib, float* v) {
+__device__ __forceinline__ void get8(const float* s, int ia, int ib, float2* v) {
   const float4 a = *reinterpret_cast<const float4*>(s + ia), b = *reinterpret_cast<const float4*>(s + ib);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  v[0] = fm::f2(a.x, a.y), v[1] = fm::f2(a.z, a.w), v[2] = fm::f2(b.x, b.y), v[3] = fm::f2(b.z, b.w);
 }
 
 template <int L>
@@ -111,28 +125,6 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-
-// Cosine and sine (times mscale; sine with the rotation's sign) of every
-// pair of the tile's tokens.
-__device__ __forceinline__ void fill_table(const Params& p, float2* tab, int first) {
-  const int half = p.rot >> 1;
-  const int per_axis = p.axes == 2 ? half >> 1 : half;
-  for (int e = threadIdx.x; e < p.tb * half; e += kThreads) {
-    const int t = e / half, i = e - t * half;
-    const int tok = first + t;
-    if (tok >= p.tokens) break;
-    const int n = tok % p.N;
-    int at = n;
-    if (p.pos != nullptr) {
-      const long long row = p.pos_batch ? tok : n;
-      at = __ldg(p.pos + row * p.axes + (i >= per_axis ? 1 : 0));
-    }
-    const double turns = (double)at * (__ldg(p.freqs + i) * 0.15915494309189533577);  // / 2 pi
-    float s, c;
-    sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-    tab[e] = make_float2(c * p.mscale, s * p.mscale * p.sign);
-  }
 }
 
 // Places of a lane's two groups of 4 elements and whether they are rotated.
@@ -149,116 +141,173 @@ __device__ __forceinline__ bool places(int lane, int rot, int& a, int& b) {
   return turned;
 }
 
-// v: the lane's elements (group a, then group b); cs: its four pairs' cosine and sine.
+// A lane's four rotations, as factors of two elements at a time: for the half
+// layout c = (c0, c1), s = (s0, s1) of neighbouring pairs, interleaved c = (c, c),
+// s = (-s, s) of one pair.
 template <bool kHalf>
-__device__ __forceinline__ void turn(float* v, const float2* cs) {
-  if constexpr (kHalf) {
+struct Turn {
+  static constexpr int kN = kHalf ? 2 : 4;
+  float2 c[kN], s[kN];
+  // of the angles with cosines x and sines y
+  __device__ __forceinline__ void set(const float* x, const float* y) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = v[i], b = v[4 + i];
-      v[i] = a * cs[i].x - b * cs[i].y;
-      v[4 + i] = b * cs[i].x + a * cs[i].y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = v[2 * i], b = v[2 * i + 1];
-      v[2 * i] = a * cs[i].x - b * cs[i].y;
-      v[2 * i + 1] = b * cs[i].x + a * cs[i].y;
+    for (int i = 0; i < kN; ++i) {
+      c[i] = kHalf ? fm::f2(x[2 * i], x[2 * i + 1]) : fm::f2(x[i], x[i]);
+      s[i] = kHalf ? fm::f2(y[2 * i], y[2 * i + 1]) : fm::f2(-y[i], y[i]);
     }
   }
-}
+  // v: the lane's elements two by two, group a then group b
+  __device__ __forceinline__ void apply(float2* v) const {
+    if constexpr (kHalf) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = v[i], b = v[2 + i];
+        const float2 bs = fm::mul2(b, s[i]);
+        v[i] = fm::fma2(a, c[i], fm::f2(-bs.x, -bs.y));
+        v[2 + i] = fm::fma2(b, c[i], fm::mul2(a, s[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fm::fma2(v[i], c[i], fm::mul2(fm::f2(v[i].y, v[i].x), s[i]));
+    }
+  }
+};
+
+// Angles of the lane's four pairs.
+struct Angles {
+  unsigned long long freq[4];  // turns per position, in units of 2^-64
+  int axis;
+  __device__ __forceinline__ void init(const Params& p, int lane) {
+    const int half = p.rot >> 1;
+    axis = p.axes == 2 && 4 * lane >= half >> 1 ? 1 : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double turns = __ldg(p.freqs + 4 * lane + e) * 0.15915494309189533577;  // / 2 pi
+      freq[e] = (unsigned long long)__double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+    }
+  }
+  // the position of token `tok` along the lane's axis
+  __device__ __forceinline__ int position(const Params& p, int tok, int n) const {
+    if (p.pos == nullptr) return n;
+    return __ldg(p.pos + (long long)(p.pos_batch ? tok : n) * p.axes + axis);
+  }
+  template <typename T, bool kHalf>
+  __device__ __forceinline__ void turn(const Params& p, int at, Turn<kHalf>* out) const {
+    float c[4], s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const unsigned long long turns = (unsigned long long)(long long)at * freq[e];  // modulo one turn
+      const float part = (float)(int)(turns >> 32);                                  // in units of 2^-32
+      if constexpr (sizeof(T) == 2)  // off by at most 2^-21.4, an 8000th of a bf16 step
+        __sincosf(part * 1.46291807926715968e-9f, &s[e], &c[e]);  // 2 pi 2^-32
+      else
+        sincospif(part * 4.656612873077392578125e-10f, &s[e], &c[e]);  // 2^-31
+      c[e] *= p.mscale;
+      s[e] *= p.mscale * p.sign;
+    }
+    out->set(c, s);
+  }
+};
+
+__device__ __forceinline__ float2 both(float x) { return fm::f2(x, x); }
 
 // v <- u, returns 1 / sqrt(...)
 template <int D, int kNorm>
-__device__ __forceinline__ float normalise(float* v, float eps) {
+__device__ __forceinline__ float normalise(float2* v, float eps) {
   constexpr int L = D / 8;
   if constexpr (kNorm == AVQ_NORM_LAYER) {
-    float s = 0.f;
+    const float2 s = fm::add2(fm::add2(v[0], v[1]), fm::add2(v[2], v[3]));
+    const float mean = group_sum<L>(s.x + s.y) * (1.f / D);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += v[i];
-    const float mean = group_sum<L>(s) * (1.f / D);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] -= mean;
+    for (int i = 0; i < 4; ++i) v[i] = fm::add2(v[i], both(-mean));
   }
-  float q = 0.f;
+  float2 q = fm::mul2(v[0], v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q += v[i] * v[i];
-  const float r = rsqrtf(group_sum<L>(q) * (1.f / D) + eps);
+  for (int i = 1; i < 4; ++i) q = fm::fma2(v[i], v[i], q);
+  const float r = rsqrtf(group_sum<L>(q.x + q.y) * (1.f / D) + eps);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= r;
+  for (int i = 0; i < 4; ++i) v[i] = fm::mul2(v[i], both(r));
   return r;
 }
 
 template <typename T, int D, int kNorm, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_kernel(const Params p) {
   constexpr int L = D / 8, G = kThreads / L, U = kBatch<T>;
-  __shared__ __align__(16) float2 tab[G * D / 2];
+  __shared__ __align__(16) typename Raw<T>::Four ring[kStages * U * 2 * kThreads];
   __shared__ __align__(16) float sw[kNorm == AVQ_NORM_NONE ? 4 : 2 * D], sb[kNorm == AVQ_NORM_NONE ? 4 : 2 * D];
   const int first = blockIdx.x * p.tb;
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int t = group & (p.tb - 1), slot = group / p.tb, slots = G / p.tb;
   const int tok = first + t;
   const bool in = tok < p.tokens;  // whole groups: the shuffles still run
-  const int b = in ? tok / p.N : 0, n = in ? tok % p.N : 0;
+  const int b = in ? tok / p.N : 0, n = in ? tok - b * p.N : 0;
   int ia, ib;
   const bool turned = places<kHalf>(lane, p.rot, ia, ib);
   // batches of U heads: the queries' first, then the keys' (the same number for every group)
   const int per = slots * U;
   const int qb = (p.H[0] + per - 1) / per, all = qb + (p.H[1] + per - 1) / per;
-  Raw<T> raw[2][U];
-  auto request = [&](int i, Raw<T>* r) {
+  const Places<T> places(ring);
+  const int apart = ib - ia;
+  auto request = [&](int i) {
     const int which = i >= qb, h0 = (which ? i - qb : i) * per + slot;
-    const T* x = static_cast<const T*>(p.x[which]) + b * p.xs[which].b + n * p.xs[which].n;
+    const int64_t sh = slots * p.xs[which].h;
+    const T* x = static_cast<const T*>(p.x[which]) + b * p.xs[which].b + n * p.xs[which].n + h0 * p.xs[which].h + ia;
+    const int left = in && i < all ? p.H[which] - h0 : 0;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int h = h0 + k * slots;
-      if (in && h < p.H[which]) r[k].load(x + h * p.xs[which].h, ia, ib);
-      else r[k].clear();
-    }
+    for (int k = 0; k < U; ++k, x += sh)
+      if (k * slots < left) places.request((i & 1) * U + k, x, apart);
+    tc::cp_async_commit();
   };
-  float2 cs[4];
-  auto finish = [&](int i, const Raw<T>* r) {
+  request(0);  // under way while the angles are made
+  request(1);
+  if constexpr (kNorm != AVQ_NORM_NONE) fill_weights<T, D>(p, sw, sb);
+  Turn<kHalf> rotation;
+  if (turned) {
+    Angles angles;
+    angles.init(p, lane);
+    angles.turn<T>(p, angles.position(p, in ? tok : 0, n), &rotation);
+  }
+  if constexpr (kNorm != AVQ_NORM_NONE) __syncthreads();
+  const long long step = (long long)slots * p.N * D;
+  for (int i = 0; i < all; ++i) {
+    tc::cp_async_wait<1>();
     const int which = i >= qb, h0 = (which ? i - qb : i) * per + slot;
-    const int H = p.H[which];
-    T* y = static_cast<T*>(p.y[which]) + ((long long)b * H * p.N + n) * D;
-    float w[8], bias[8];
+    const int H = p.H[which], left = in ? H - h0 : 0;
+    T* y = static_cast<T*>(p.y[which]) + (((long long)b * H + h0) * p.N + n) * D + ia;
+    float2 w[4], bias[4];
     if constexpr (kNorm != AVQ_NORM_NONE) {
       get8(sw + which * D, ia, ib, w);
       get8(sb + which * D, ia, ib, bias);
     }
+    float2 v[U][4];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int h = h0 + k * slots;
-      float v[8];
-      r[k].get(v);
+      places.get((i & 1) * U + k, v[k]);  // of an absent head: anything, never stored
       if constexpr (kNorm != AVQ_NORM_NONE) {
-        normalise<D, kNorm>(v, p.eps);
+        normalise<D, kNorm>(v[k], p.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * w[e] + bias[e];
-      }
-      if (turned) turn<kHalf>(v, cs);
-      if (in && h < H) {
-        store4(y + (long long)h * p.N * D + ia, v);
-        store4(y + (long long)h * p.N * D + ib, v + 4);
+        for (int e = 0; e < 4; ++e) v[k][e] = fm::fma2(v[k][e], w[e], bias[e]);
       }
     }
-  };
-  request(0, raw[0]);  // under way while the table is made
-  fill_table(p, tab, first);
-  if constexpr (kNorm != AVQ_NORM_NONE) fill_weights<T, D>(p, sw, sb);
-  __syncthreads();
-  if (turned) {
+    if (turned) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = tab[t * (p.rot >> 1) + 4 * lane + i];
-  }
-  for (int i = 0; i < all; i += 2) {
-    if (i + 1 < all) request(i + 1, raw[1]);
-    finish(i, raw[0]);
-    if (i + 1 < all) {
-      if (i + 2 < all) request(i + 2, raw[0]);
-      finish(i + 1, raw[1]);
+      for (int k = 0; k < U; ++k) rotation.apply(v[k]);
     }
+    if ((U - 1) * slots < left) {
+#pragma unroll
+      for (int k = 0; k < U; ++k, y += step) {
+        store4(y, v[k]);
+        store4(y + apart, v[k] + 2);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < U; ++k, y += step)
+        if (k * slots < left) {
+          store4(y, v[k]);
+          store4(y + apart, v[k] + 2);
+        }
+    }
+    request(i + 2);
   }
 }
 
@@ -268,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_kernel(const Params p) {
 template <typename T, int D, int kNorm, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Params p, int tiles) {
   constexpr int L = D / 8, G = kThreads / L, U = kBatch<T> / 2;
-  __shared__ __align__(16) float2 tab[2][G * D / 2];
-  __shared__ float sums[G][D];
+  __shared__ __align__(16) typename Raw<T>::Four ring[kStages * U * 4 * kThreads];
+  float* sums = reinterpret_cast<float*>(ring);  // [G][D], at the end
   const int which = blockIdx.y;
   const int H = p.H[which];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -277,112 +326,156 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Par
   int ia, ib;
   const bool turned = places<kHalf>(lane, p.rot, ia, ib);
   const Strides xs = p.xs[which], gs = p.gs[which];
-  float w[8], dw[8], db[8];
+  float2 w[4], dw[4], db[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 1.f, dw[i] = 0.f, db[i] = 0.f;
+  for (int i = 0; i < 4; ++i) w[i] = both(1.f), dw[i] = db[i] = both(0.f);
   if (p.w[which] != nullptr) {
-    loadE<4>(static_cast<const T*>(p.w[which]) + ia, w);
-    loadE<4>(static_cast<const T*>(p.w[which]) + ib, w + 4);
+    const T* pw = static_cast<const T*>(p.w[which]);
+    typedef typename Raw<T>::Four Four;
+    Raw<T>::get(*reinterpret_cast<const Four*>(pw + ia), *reinterpret_cast<const Four*>(pw + ib), w);
   }
   // batches of U heads of a tile's tokens, tile after tile
   const int per = slots * U, batches = (H + per - 1) / per;
-  Raw<T> rx[2][U], rg[2][U];
-  auto request = [&](int tile, int i, Raw<T>* x, Raw<T>* g) {
+  const int apart = ib - ia;
+  const int64_t x_step = slots * xs.h, g_step = slots * gs.h;
+  const long long y_step = (long long)slots * p.N * D;
+  const Places<T> places(ring);
+  Angles angles;
+  if (turned) angles.init(p, lane);
+  // a batch: where the group's token stands at the group's first head of it
+  struct At {
+    const T *x, *g;
+    T* y;
+    int left;  // heads from there on, 0 for a token past the end
+    int tile, i, pos;
+  };
+  auto first_of = [&](int tile) {
     const int tok = tile * p.tb + t;
-    const bool in = tok < p.tokens;
-    const int b = in ? tok / p.N : 0, n = in ? tok % p.N : 0;
-    const T* px = static_cast<const T*>(p.x[which]) + b * xs.b + n * xs.n;
-    const T* pg = static_cast<const T*>(p.g[which]) + b * gs.b + n * gs.n;
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int h = i * per + k * slots + slot;
-      if (in && h < H) {
-        x[k].load(px + h * xs.h, ia, ib);
-        g[k].load(pg + h * gs.h, ia, ib);
-      } else {
-        x[k].clear();
-        g[k].clear();
-      }
+    const bool in = tile < tiles && tok < p.tokens;
+    const int b = in ? tok / p.N : 0, n = in ? tok - b * p.N : 0;
+    At at;
+    at.x = static_cast<const T*>(p.x[which]) + b * xs.b + n * xs.n + slot * xs.h + ia;
+    at.g = static_cast<const T*>(p.g[which]) + b * gs.b + n * gs.n + slot * gs.h + ia;
+    at.y = static_cast<T*>(p.y[which]) + (((long long)b * H + slot) * p.N + n) * D + ia;
+    at.left = in ? H - slot : 0;
+    at.tile = tile;
+    at.i = 0;
+    at.pos = turned ? angles.position(p, in ? tok : 0, n) : 0;
+    return at;
+  };
+  auto advance = [&](At& at) {
+    if (++at.i == batches) {
+      at = first_of(at.tile + gridDim.x);
+    } else {
+      at.x += U * x_step;
+      at.g += U * g_step;
+      at.y += U * y_step;
+      at.left -= U * slots;
     }
   };
-  float2 cs[4];
-  auto finish = [&](int tile, int i, const Raw<T>* rx, const Raw<T>* rg) {
-    const int tok = tile * p.tb + t;
-    const bool in = tok < p.tokens;
-    const int b = in ? tok / p.N : 0, n = in ? tok % p.N : 0;
-    T* y = static_cast<T*>(p.y[which]) + ((long long)b * H * p.N + n) * D;
+  auto request = [&](const At& at, int stage) {
+    const T *px = at.x, *pg = at.g;
+#pragma unroll
+    for (int k = 0; k < U; ++k, px += x_step, pg += g_step) {
+      if (k * slots >= at.left) continue;
+      places.request((stage * U + k) * 2, px, apart);
+      places.request((stage * U + k) * 2 + 1, pg, apart);
+    }
+    tc::cp_async_commit();
+  };
+  Turn<kHalf> rotation;
+  auto finish = [&](T* y, int left, int stage) {
+    float2 u[U][4], z[U][4];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int h = i * per + k * slots + slot;
-      const bool live = in && h < H;
-      float u[8], z[8];
-      rx[k].get(u);
-      rg[k].get(z);
-      if (turned) turn<kHalf>(z, cs);
-      const float r = normalise<D, kNorm>(u, p.eps);
-      float gu = 0.f, gm = 0.f;
+      places.get((stage * U + k) * 2, u[k]);
+      places.get((stage * U + k) * 2 + 1, z[k]);
+    }
+    const bool whole = (U - 1) * slots < left;
+    if (!whole) {  // an absent row is 0 throughout
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (live) {  // an absent row's u is 0 / 0 when eps is 0
-          dw[e] += z[e] * u[e];
-          db[e] += z[e];
+      for (int k = 0; k < U; ++k)
+        if (k * slots >= left) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[k][e] = z[k][e] = both(0.f);
         }
-        z[e] *= w[e];
-        gu += z[e] * u[e];
-        gm += z[e];
-      }
-      gu = group_sum<L>(gu) * (1.f / D);
-      gm = kNorm == AVQ_NORM_LAYER ? group_sum<L>(gm) * (1.f / D) : 0.f;
-      if (live) {
+    }
+    if (turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = (z[e] - gm - u[e] * gu) * r;
-        store4(y + (long long)h * p.N * D + ia, z);
-        store4(y + (long long)h * p.N * D + ib, z + 4);
-      }
+      for (int k = 0; k < U; ++k) rotation.apply(z[k]);
     }
-  };
-  // the batch after (tile, i)
-  auto next = [&](int& tile, int& i) {
-    if (++i == batches) {
-      i = 0;
-      tile += gridDim.x;
-    }
-  };
-  int tile = blockIdx.x, i = 0, made = 0;
-  if (tile < tiles) request(tile, i, rx[0], rg[0]);
-  // one turn of the loop handles two batches, so that the buffers' places are known
-  auto turn_of = [&](int cur) {
-    int nt = tile, ni = i;
-    next(nt, ni);
-    if (nt < tiles) request(nt, ni, rx[cur ^ 1], rg[cur ^ 1]);
-    if (i == 0) {  // a new tile: its sines and cosines, in the table that no one reads any more
-      fill_table(p, tab[made & 1], tile * p.tb);
-      __syncthreads();
-      if (turned) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) cs[e] = tab[made & 1][t * (p.rot >> 1) + 4 * lane + e];
+    for (int k = 0; k < U; ++k) {
+      const float r = normalise<D, kNorm>(u[k], whole || k * slots < left ? p.eps : 1.f);
+      float2 gu = both(0.f), gm = both(0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dw[e] = fm::fma2(z[k][e], u[k][e], dw[e]);
+        db[e] = fm::add2(db[e], z[k][e]);
+        z[k][e] = fm::mul2(z[k][e], w[e]);
+        gu = fm::fma2(z[k][e], u[k][e], gu);
+        if constexpr (kNorm == AVQ_NORM_LAYER) gm = fm::add2(gm, z[k][e]);
       }
-      ++made;
+      const float mu = group_sum<L>(gu.x + gu.y) * (-1.f / D);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[k][e] = fm::fma2(u[k][e], both(mu), z[k][e]);
+      if constexpr (kNorm == AVQ_NORM_LAYER) {
+        const float mean = group_sum<L>(gm.x + gm.y) * (-1.f / D);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[k][e] = fm::add2(z[k][e], both(mean));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[k][e] = fm::mul2(z[k][e], both(r));
     }
-    finish(tile, i, rx[cur], rg[cur]);
-    tile = nt;
-    i = ni;
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < U; ++k, y += y_step) {
+        store4(y, z[k]);
+        store4(y + apart, z[k] + 2);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < U; ++k, y += y_step)
+        if (k * slots < left) {
+          store4(y, z[k]);
+          store4(y + apart, z[k] + 2);
+        }
+    }
   };
-  while (tile < tiles) {
+  // the batch that is worked on is two behind the one that is requested
+  At ahead = first_of(blockIdx.x);
+  T* y[2];
+  int left[2], pos[2], state[2];  // state: 0 further batch of a tile, 1 its first, 2 past the end
+  auto ask = [&](int stage) {
+    request(ahead, stage);
+    y[stage] = ahead.y;
+    left[stage] = ahead.left;
+    pos[stage] = ahead.pos;
+    state[stage] = ahead.tile >= tiles ? 2 : ahead.i == 0;
+    advance(ahead);
+  };
+  auto turn_of = [&](int stage) {
+    if (state[stage] == 1 && turned) angles.turn<T>(p, pos[stage], &rotation);
+    tc::cp_async_wait<1>();
+    finish(y[stage], left[stage], stage);
+    ask(stage);
+  };
+  ask(0);
+  ask(1);
+  while (state[0] < 2) {
     turn_of(0);
-    if (tile < tiles) turn_of(1);
+    if (state[1] == 2) break;
+    turn_of(1);
   }
+  tc::cp_async_wait<0>();
   for (int kind = 0; kind < 2; ++kind) {
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sums[group][ia + i] = kind == 0 ? dw[i] : db[i];
-      sums[group][ib + i] = kind == 0 ? dw[4 + i] : db[4 + i];
-    }
+    store4(sums + group * D + ia, kind == 0 ? dw : db);
+    store4(sums + group * D + ib, kind == 0 ? dw + 2 : db + 2);
     __syncthreads();
     if (threadIdx.x < D) {
       float s = 0.f;
-      for (int k = 0; k < G; ++k) s += sums[k][threadIdx.x];
+      for (int k = 0; k < G; ++k) s += sums[k * D + threadIdx.x];
       p.part[(((size_t)which * gridDim.x + blockIdx.x) * 2 + kind) * D + threadIdx.x] = s;
     }
   }
@@ -470,7 +563,7 @@ int backward_blocks(const avq_qk_dims& s) {
   const int tokens = s.B * s.N;
   const int tb = tile_tokens(s.d, tokens);
   const int tiles = (tokens + tb - 1) / tb;
-  const int most = 2 * num_sms();  // for each of queries and keys: four blocks per SM in all
+  const int most = s.Hk > 0 ? num_sms() : 2 * num_sms();  // the two blocks that an SM holds
   return tiles < most ? tiles : most;
 }
 
