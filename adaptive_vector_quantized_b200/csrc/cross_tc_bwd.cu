@@ -96,16 +96,14 @@ __device__ __forceinline__ void mma_rows_rows(uint32_t d, uint64_t a, uint64_t b
     tc::mma_bf16(d, a + off, b + off, idesc, k > 0);
   }
 }
-// D[128 x D] (+)= A[128][16 steps] B[16 steps][D]: A in TMEM (two halves of 4
+// D[128 x D] (+)= A[128][128] B[128][D]: A in TMEM (two halves of 4
 // steps, 64 columns apart), B a tile of rows in shared memory
 template <int D>
-__device__ __forceinline__ void mma_tmem_cols(uint32_t d, uint32_t a, uint64_t b, int steps, uint32_t more) {
+__device__ __forceinline__ void mma_tmem_cols(uint32_t d, uint32_t a, uint64_t b, uint32_t more) {
   constexpr uint32_t idesc = tc::idesc_bf16(128, D, 0, 1);
-#pragma unroll 1
-  for (int k = 0; k < steps; ++k) {
-    tc::mma_bf16_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, b + k * (2048 >> 4), idesc, more);
-    more = 1;
-  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    tc::mma_bf16_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, b + k * (2048 >> 4), idesc, k > 0 ? 1 : more);
 }
 
 // p = exp2(c2 s + nl) for 32 scores; packed to bf16 in out
@@ -312,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           if (!ok) break;
           tc::tc_fence_after();
           if (lane == 0) {
-            mma_tmem_cols<D>(tV, tS, ring_mn + gs * kTile16, 8, j > x.i0);  // dV += P^T dO
+            mma_tmem_cols<D>(tV, tS, ring_mn + gs * kTile16, j > x.i0);  // dV += P^T dO
             tc::mma_commit(bar.empty + gs);
             if (!last) {
               mma_rows_rows<D>(tS, own, ring + (n + 2) % S::kSlots * kTile16);
@@ -325,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           if (!ok) break;
           tc::tc_fence_after();
           if (lane == 0) {
-            mma_tmem_cols<D>(tK, tP, ring_mn + qs * kTile16, 8, j > x.i0);  // dK += dS^T Q
+            mma_tmem_cols<D>(tK, tP, ring_mn + qs * kTile16, j > x.i0);  // dK += dS^T Q
             tc::mma_commit(bar.empty + qs);
             if (!last) {
               mma_rows_rows<D>(tP, own + kTile16, ring + (n + 3) % S::kSlots * kTile16);
@@ -578,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
           if (!ok) break;
           tc::tc_fence_after();
           if (lane == 0) {
-            mma_tmem_cols<D>(tQ, tP, ring_mn + ks * kTile16, 8, j > x.t0);  // dQ += dS K
+            mma_tmem_cols<D>(tQ, tP, ring_mn + ks * kTile16, j > x.t0);  // dQ += dS K
             tc::mma_commit(bar.empty + ks);
             if (!last) {
               const uint32_t vs = (n + 3) % S::kSlots;
