@@ -5,8 +5,8 @@
 //
 // A block works on pairs of 128-row tiles of one head; both tiles share every
 // K and V tile that TMA brings through a ring in shared memory.  One warp loads,
-// one clears V's rows of keys that are left out, one thread of two others issues
-// the MMAs of a tile each, two groups of four warps do the softmax, a row to a
+// one clears V's rows of keys that are left out, two issue the MMAs of a tile
+// each, two groups of four warps do the softmax, a row to a
 // thread.  S and O stay in TMEM; P overwrites its S there (bf16, two to a
 // column) and is the first operand of P V straight from TMEM.
 //
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   uint64_t* drain = tail + 2;
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kBars; ++i) {
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         have = true;
       }
       if (have && ok) pass(&last, last.t1 - 1);
-    } else if (lane == 0) {
-      // One thread issues the MMAs of one tile of the pairs.  A turn of the loop
+    } else {
+      // One warp issues the MMAs of one tile of the pairs.  A turn of the loop
       // takes a unit of the ring: by halves, P V of the key tile `cur` and behind
       // it S of the tile `next`, into the same half of S.  So S is there a step
       // ahead of the softmax.  The pipe holds only a few MMAs: whatever else the
@@ -252,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       auto settle = [&] {                                             // the first tile at or after item i
         for (; i < items; i += gridDim.x) {
           const Item x = item_of(a, i, pairs);
-          t0 = j = x.t0;
-          t1 = x.t1;
-          count = x.count;
+          t0 = j = uniform(x.t0);
+          t1 = uniform(x.t1);
+          count = uniform(x.count);
           on = t < x.tiles;
           left = min(kKeyTile, count - j * kKeyTile);
           if (t0 < t1) return true;
@@ -267,34 +267,36 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       uint32_t add = 0, slot = 0, phase = 0, buf = 0, q_phase = 0, p_phase = 0;  // p_phase: bit h for half h
       bool ok = true;
       while (cur_left > 0 || more) {
-        ok = guard.wait(ready + slot, phase);
+        ok = wait_all(guard, ready + slot, phase);
         if (!ok) break;
         const bool fresh = j == t0, next_on = more && on, next_last = j + 1 == t1;
-        if (next_on && fresh) ok = guard.wait(q_full + 2 * buf + t, q_phase);
+        if (next_on && fresh) ok = wait_all(guard, q_full + 2 * buf + t, q_phase);
         if (!ok) break;
         const uint64_t vd = ring + slot * kUnit16, kd = ring_k + slot * kUnit16, qd = qtile + buf * 2 * kTile16;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t s = tS(t, half);
           if (cur_on && cur_left > half * kStep) {
-            ok = guard.wait(my_p + half, p_phase >> half & 1);
+            ok = wait_all(guard, my_p + half, p_phase >> half & 1);
             if (!ok) break;
             p_phase ^= 1u << half;
             tc::tc_fence_after();
-            if (cur_left >= (half + 1) * kStep) {
+            if (tc::elect_one()) {
+              if (cur_left >= (half + 1) * kStep) {
 #pragma unroll
-              for (int k = 0; k < kStep / 16; ++k)
-                tc::mma_bf16_ts(o, s + k * 8, vd + half * kHalf16 + k * (2048 >> 4), idesc_o,
-                                half > 0 || k > 0 ? 1 : add);
-            } else {
-              for (int k = 0; k * 16 < cur_left - half * kStep; ++k)
-                tc::mma_bf16_ts(o, s + k * 8, vd + half * kHalf16 + k * (2048 >> 4), idesc_o,
-                                half > 0 || k > 0 ? 1 : add);
-            }
-            if (cur_last && cur_left <= (half + 1) * kStep) {
-              tc::mma_commit(o_full + t);
-            } else if (half == 0 ? cur_last : next_on && !fresh && next_last && left <= kStep) {
-              tc::mma_commit(tail + t);
+                for (int k = 0; k < kStep / 16; ++k)
+                  tc::mma_bf16_ts(o, s + k * 8, vd + half * kHalf16 + k * (2048 >> 4), idesc_o,
+                                  half > 0 || k > 0 ? 1 : add);
+              } else {
+                for (int k = 0; k * 16 < cur_left - half * kStep; ++k)
+                  tc::mma_bf16_ts(o, s + k * 8, vd + half * kHalf16 + k * (2048 >> 4), idesc_o,
+                                  half > 0 || k > 0 ? 1 : add);
+              }
+              if (cur_last && cur_left <= (half + 1) * kStep) {
+                tc::mma_commit(o_full + t);
+              } else if (half == 0 ? cur_last : next_on && !fresh && next_last && left <= kStep) {
+                tc::mma_commit(tail + t);
+              }
             }
           }
           if (next_on && left > half * kStep) {
@@ -302,16 +304,18 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
                 left >= (half + 1) * kStep
                     ? tc::idesc_bf16(kRowTile, kStep, 0, 0)
                     : tc::idesc_bf16(kRowTile, 0, 0, 0) + (uint32_t)((left - half * kStep + 15) >> 4 << 1 << 17);
+            if (tc::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int off = ((k >> 2) * (kRowTile * 128) + (k & 3) * 32) >> 4;
-              tc::mma_bf16(s, qd + off, kd + half * kHalf16 + off, idesc, k > 0);
+              for (int k = 0; k < D / 16; ++k) {
+                const int off = ((k >> 2) * (kRowTile * 128) + (k & 3) * 32) >> 4;
+                tc::mma_bf16(s, qd + off, kd + half * kHalf16 + off, idesc, k > 0);
+              }
+              tc::mma_commit(my_s + half);
             }
-            tc::mma_commit(my_s + half);
           }
         }
         if (!ok) break;
-        tc::mma_commit(empty + slot);
+        if (tc::elect_one()) tc::mma_commit(empty + slot);
         if (++slot == S::kUnits) {
           slot = 0;
           phase ^= 1;
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           ++j;
           left = min(kKeyTile, count - j * kKeyTile);
           if (j == t1) {
-            tc::mma_commit(q_empty + buf);
+            if (tc::elect_one()) tc::mma_commit(q_empty + buf);
             if (++buf == S::kQBufs) {
               buf = 0;
               q_phase ^= 1;
@@ -335,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         }
       }
       // every MMA done before TMEM is given back
-      tc::mma_commit(drain + t);
+      if (tc::elect_one()) tc::mma_commit(drain + t);
+      __syncwarp();
       tc::mbar_wait(drain + t, 0, 1000000ull);
     }
   } else {

@@ -30,6 +30,14 @@ struct Guard {
   }
 };
 
+// The same for a warp as a whole: all its lanes agree, so that the compiler can
+// keep what follows in uniform registers.
+__device__ __forceinline__ bool wait_all(const Guard& g, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, g.wait(bar, parity));
+}
+// A value that every lane holds, known to the compiler as such.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Bit i of word w: key k0 + 32 w + i is looked at.  All lanes get all words.
 struct KeyBits {
   uint32_t w[4];

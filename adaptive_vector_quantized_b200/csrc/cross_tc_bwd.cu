@@ -8,12 +8,18 @@
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
 //
 // A block has two groups of four warps for the elementwise work (a TMEM lane to
-// a thread, half of the tile's columns to a group), a warp that issues MMAs, one
-// that loads by TMA and one that fetches lse and delta.  P and dS overwrite S
-// and dP in TMEM as bf16 and are first operands from there.  Elementwise work
-// and MMAs alternate in two phases that overlap:
-//   dK/dV:  P(j) | dK(j-1), dP(j)      dS(j) | dV(j), S(j+1)
-//   dQ:     P(j) | dQ(j-1), dP(j)      dS(j) | S(j+1)
+// a thread, half of the tile's columns to a group), a warp that loads by TMA, one
+// that fetches lse and delta (dK/dV) or clears K's rows of keys that are left
+// out (dQ), and two threads that issue the MMAs of a chain each, since what a
+// thread does between MMAs would leave the tensor pipe idle.  P and dS overwrite
+// S and dP in TMEM as bf16 and are first operands from there.
+//   dK/dV:  S(j) -> P(j) -> dV(j), S(j+1)     dP(j) -> dS(j) -> dK(j), dP(j+1)
+//   dQ:     S(j), S(j+1) in turn              dP(j) -> dS(j) -> dQ(j), dP(j+1)
+// For dK and dV the chains run apart for the two groups' halves of a tile, so
+// that one group works while the MMAs of the other's half do (8192 rows x 4096
+// keys, 8 heads of 128 on 4: 298 us against 312); for dQ, whose S is a step ahead
+// anyhow, whole tiles are better (233 us against 246): a product with 64 columns
+// takes 48 clocks of shared memory reads, one with 128 takes 64.
 #include "cross_tc.cuh"
 
 namespace avq {
@@ -21,7 +27,8 @@ namespace avq {
 namespace {
 
 constexpr int kWorkWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kRowWarp = 10;
+constexpr int kMmaWarp = 8;  // and the next: the chain of S, the chain of dP
+constexpr int kLoadWarp = 10, kHelpWarp = 11;
 constexpr int kThreads = 384;
 // registers: 168 a thread at launch, then 2 * 216 + 72 = 3 * 168
 constexpr int kWorkRegs = 216, kOtherRegs = 72;
@@ -30,47 +37,81 @@ template <int D>
 struct Smem {
   static constexpr int kBlocks = D / 64;
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kSlots = 4;                          // ring of the walked tiles
-  static constexpr int kOwn = 0;                            // the block's own two tiles; results staged there
-  static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kRows = kRing + kSlots * kTileBytes; // [2 stages][lse, delta][128]
+  // Rings of the walked tiles: the first of each pair (Q, or K) is held from the
+  // product of its S to that of the gradient, the second (dO, or V) for less.
+  static constexpr int kSlotsA = 3, kSlotsB = 2;
+  static constexpr int kOwn = 0;  // the block's own two tiles; results staged there
+  static constexpr int kRingA = 2 * kTileBytes;
+  static constexpr int kRingB = kRingA + kSlotsA * kTileBytes;
+  static constexpr int kRows = kRingB + kSlotsB * kTileBytes;  // [2 stages][lse, delta][128]
   static constexpr int kBar = kRows + 2 * 1024;
-  // full[slots], empty[slots], own_full, own_empty, s_full[2], dp_full, p_ready, ds_ready, done, rows_full[2],
-  // rows_empty[2], drain
-  static constexpr int kBars = 2 * kSlots + 13;
+  // a_full[3], a_empty[3], a_ready[3], b_full[2], b_empty[2], own_full, own_empty, s_full[2], dp_full[2], p_ready[2],
+  // ds_ready[2], done, rows_full[2], rows_empty[2], drain[2]
+  static constexpr int kBars = 3 * kSlotsA + 2 * kSlotsB + 17;
   static constexpr int kMisc = kBar + kBars * 8;
   static constexpr int kTotal = kMisc + 16;
 };
 
 struct Bars {
-  uint64_t *full, *empty, *own_full, *own_empty, *s_full, *dp_full, *p_ready, *ds_ready, *done, *rows_full,
-      *rows_empty, *drain;
+  uint64_t *a_full, *a_empty, *a_ready, *b_full, *b_empty, *own_full, *own_empty, *s_full, *dp_full, *p_ready,
+      *ds_ready, *done, *rows_full, *rows_empty, *drain;
 };
 template <int D>
 __device__ __forceinline__ Bars bars_of(uint8_t* sm) {
+  using S = Smem<D>;
   Bars b;
-  b.full = reinterpret_cast<uint64_t*>(sm + Smem<D>::kBar);
-  b.empty = b.full + Smem<D>::kSlots;
-  b.own_full = b.empty + Smem<D>::kSlots;
+  b.a_full = reinterpret_cast<uint64_t*>(sm + S::kBar);
+  b.a_empty = b.a_full + S::kSlotsA;
+  b.a_ready = b.a_empty + S::kSlotsA;
+  b.b_full = b.a_ready + S::kSlotsA;
+  b.b_empty = b.b_full + S::kSlotsB;
+  b.own_full = b.b_empty + S::kSlotsB;
   b.own_empty = b.own_full + 1;
   b.s_full = b.own_empty + 1;
   b.dp_full = b.s_full + 2;
-  b.p_ready = b.dp_full + 1;
-  b.ds_ready = b.p_ready + 1;
-  b.done = b.ds_ready + 1;
+  b.p_ready = b.dp_full + 2;
+  b.ds_ready = b.p_ready + 2;
+  b.done = b.ds_ready + 2;
   b.rows_full = b.done + 1;
   b.rows_empty = b.rows_full + 2;
   b.drain = b.rows_empty + 2;
   return b;
 }
+// A ring's slot and phase, stepped along.
+template <int kSlots>
+struct Turn {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// b_users: threads that release a slot of the second ring; p_warps: warps that
+// arrive at a p_ready; done_users: threads whose last MMAs complete an item.
 template <int D>
-__device__ __forceinline__ void init_bars(const Bars& b) {
+__device__ __forceinline__ void init_bars(const Bars& b, int b_users, int p_warps, int done_users) {
   for (int i = 0; i < Smem<D>::kBars; ++i) {
-    uint64_t* x = b.full + i;
-    const bool all = x == b.own_empty || x == b.p_ready || x == b.ds_ready || x == b.rows_empty || x == b.rows_empty + 1;
-    tc::mbar_init(x, all ? kWorkWarps : 1);
+    uint64_t* x = b.a_full + i;
+    uint32_t n = 1;
+    if (x == b.own_empty || (x >= b.rows_empty && x < b.drain)) n = kWorkWarps;
+    if (x >= b.b_empty && x < b.own_full) n = b_users;
+    if (x >= b.p_ready && x < b.ds_ready) n = p_warps;
+    if (x >= b.ds_ready && x < b.done) n = kWorkWarps / 2;
+    if (x == b.done) n = done_users;
+    tc::mbar_init(x, n);
   }
   tc::fence_mbar_init();
+}
+
+// Waits, with a limit, for the last load into each slot of a ring (`loads` in
+// all; t: the turn after the last): nothing may be in flight when a block ends.
+template <int kSlots>
+__device__ __forceinline__ void drain_ring(uint64_t* full, Turn<kSlots> t, uint32_t loads) {
+  for (uint32_t k = 0; k < kSlots; ++k, t.step())  // t.slot: the slot whose last load is oldest
+    if (loads + k >= kSlots) tc::mbar_wait(full + t.slot, t.phase ^ 1, 1000000ull);
 }
 
 struct Maps {
@@ -86,25 +127,24 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
     tc::tma_load_4d(dst + c * 128 * 128, map, c * 64, row, st.h != 0 ? h : 0, st.b != 0 ? b : 0, bar);
 }
 
-// D[128 x 128] = A[128][D] B[128][D]^T, both tiles of rows in shared memory
-template <int D>
+// D[128 x N] = A[128][D] B[N][D]^T, both tiles of rows in shared memory
+template <int D, int N>
 __device__ __forceinline__ void mma_rows_rows(uint32_t d, uint64_t a, uint64_t b) {
-  constexpr uint32_t idesc = tc::idesc_bf16(128, 128, 0, 0);
+  constexpr uint32_t idesc = tc::idesc_bf16(128, N, 0, 0);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     const int off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
     tc::mma_bf16(d, a + off, b + off, idesc, k > 0);
   }
 }
-// D[128 x D] (+)= A[128][128] B[128][D]: A in TMEM (two halves of 4
-// steps, 64 columns apart), B a tile of rows in shared memory
+// D[128 x D] (+)= A[128][64] B[64][D]: A in TMEM, B rows of a tile in shared memory
 template <int D>
 __device__ __forceinline__ void mma_tmem_cols(uint32_t d, uint32_t a, uint64_t b, uint32_t more) {
   constexpr uint32_t idesc = tc::idesc_bf16(128, D, 0, 1);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    tc::mma_bf16_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, b + k * (2048 >> 4), idesc, k > 0 ? 1 : more);
+  for (int k = 0; k < 4; ++k) tc::mma_bf16_ts(d, a + k * 8, b + k * (2048 >> 4), idesc, k > 0 ? 1 : more);
 }
+constexpr int kHalf16 = 64 * 128 >> 4;  // from a tile's row 0 to its row 64, in units of a descriptor
 
 // p = exp2(c2 s + nl) for 32 scores; packed to bf16 in out
 template <bool kVec>
@@ -197,15 +237,18 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
                                                                   const CrossArgs a, unsigned int* err, int items,
                                                                   int ktiles, int rtiles) {
   using S = Smem<D>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (tc::smem_u32(sm) & 1023u) {  // no room is left to align it here
+    if (threadIdx.x == 0) atomicOr(err, kErrInternal);
+    return;
+  }
   const Bars bar = bars_of<D>(sm);
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
   float* sRows = reinterpret_cast<float*>(sm + S::kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    init_bars<D>(bar);
+    init_bars<D>(bar, 2, kWorkWarps / 2, 2);
     *sAbort = 0;
   }
   if (warp == kMmaWarp) {
@@ -223,7 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
     tc::regs_give<kOtherRegs>();
     if (warp == kLoadWarp) {
       if (lane == 0) {
-        uint32_t n = 0, own = 0;
+        Turn<S::kSlotsA> ta;
+        Turn<S::kSlotsB> tb;
+        uint32_t na = 0, nb = 0, own = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
           const KeyItem x = key_item(a, i, ktiles, rtiles);
@@ -234,22 +279,29 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           load_tile<D>(sm + S::kOwn, &maps.k, a.ks, x.k0, x.kh, x.kb, bar.own_full);
           load_tile<D>(sm + S::kOwn + S::kTileBytes, &maps.v, a.vs, x.k0, x.kh, x.kb, bar.own_full);
           ++own;
-          for (long long j = 2 * x.i0; j < 2 * x.i1; ++j, ++n) {  // Q, then dO of each row tile
-            const RowTile r = row_tile(a, x, j >> 1, rtiles);
-            const int slot = n % S::kSlots;
-            ok = guard.wait(bar.empty + slot, (n / S::kSlots & 1) ^ 1);
+          for (long long j = x.i0; j < x.i1; ++j) {
+            const RowTile r = row_tile(a, x, j, rtiles);
+            ok = guard.wait(bar.a_empty + ta.slot, ta.phase ^ 1);
             if (!ok) break;
-            tc::mbar_arrive_expect_tx(bar.full + slot, S::kTileBytes);
-            const bool g = j & 1;
-            load_tile<D>(sm + S::kRing + slot * S::kTileBytes, g ? &maps.g : &maps.q, g ? a.gs : a.qs, r.row0, r.h,
-                         r.b, bar.full + slot);
+            tc::mbar_arrive_expect_tx(bar.a_full + ta.slot, S::kTileBytes);
+            load_tile<D>(sm + S::kRingA + ta.slot * S::kTileBytes, &maps.q, a.qs, r.row0, r.h, r.b,
+                         bar.a_full + ta.slot);
+            ta.step();
+            ++na;
+            ok = guard.wait(bar.b_empty + tb.slot, tb.phase ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(bar.b_full + tb.slot, S::kTileBytes);
+            load_tile<D>(sm + S::kRingB + tb.slot * S::kTileBytes, &maps.g, a.gs, r.row0, r.h, r.b,
+                         bar.b_full + tb.slot);
+            tb.step();
+            ++nb;
           }
         }
-        for (uint32_t k = n > S::kSlots ? n - S::kSlots : 0; k < n; ++k)
-          tc::mbar_wait(bar.full + k % S::kSlots, k / S::kSlots & 1, 1000000ull);
+        drain_ring(bar.a_full, ta, na);
+        drain_ring(bar.b_full, tb, nb);
         if (own > 0) tc::mbar_wait(bar.own_full, (own - 1) & 1, 1000000ull);
       }
-    } else if (warp == kRowWarp) {
+    } else if (warp == kHelpWarp) {
       uint32_t n = 0;
       bool ok = true;
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
@@ -277,67 +329,76 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           if (lane == 0) tc::mbar_arrive(bar.rows_full + (n & 1));
         }
       }
-    } else if (warp == kMmaWarp) {
+    } else if (lane == 0) {
+      const bool second = warp > kMmaWarp;  // the chain of dP
       const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
-      const uint64_t ring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 16, 1024);
-      const uint64_t ring_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 128 * 128, 1024);
+      const uint64_t ring_a = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingA), 16, 1024);
+      const uint64_t ring_b = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingB), 16, 1024);
+      const uint64_t ring_a_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingA), 128 * 128, 1024);
+      const uint64_t ring_b_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingB), 128 * 128, 1024);
       constexpr int kTile16 = S::kTileBytes >> 4;
-      uint32_t n = 0, own_n = 0, steps = 0;
+      Turn<S::kSlotsA> ta;  // Q and dO of the row tile whose gradients are next,
+      Turn<S::kSlotsB> tb;
+      Turn<S::kSlotsA> ta1;  // and of the one whose S and dP are
+      Turn<S::kSlotsB> tb1;
+      uint32_t own_n = 0, steps = 0;
       bool ok = true;
+      // S^T = K Q^T or dP^T = V dO^T of half a row tile's rows
+      auto form = [&](int half) {
+        const uint32_t d = (second ? tP : tS) + half * 64;
+        if (!second) {
+          if (half == 0 && !guard.wait(bar.a_full + ta1.slot, ta1.phase)) return false;
+          mma_rows_rows<D, 64>(d, own, ring_a + ta1.slot * kTile16 + half * kHalf16);
+          tc::mma_commit(bar.s_full + half);
+          if (half == 1) ta1.step();
+        } else {
+          if (half == 0 && !guard.wait(bar.b_full + tb1.slot, tb1.phase)) return false;
+          mma_rows_rows<D, 64>(d, own + kTile16, ring_b + tb1.slot * kTile16 + half * kHalf16);
+          tc::mma_commit(bar.dp_full + half);
+          if (half == 1) {
+            tc::mma_commit(bar.b_empty + tb1.slot);  // dO: the chain of S releases it too
+            tb1.step();
+          }
+        }
+        return true;
+      };
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const KeyItem x = key_item(a, i, ktiles, rtiles);
         if (x.i0 >= x.i1) continue;
-        ok = guard.wait(bar.own_full, own_n & 1) && guard.wait(bar.full + n % S::kSlots, n / S::kSlots & 1);
+        ok = guard.wait(bar.own_full, own_n & 1) && form(0) && form(1);
         if (!ok) break;
         ++own_n;
-        if (lane == 0) {
-          mma_rows_rows<D>(tS, own, ring + n % S::kSlots * kTile16);  // S^T = K Q^T
-          tc::mma_commit(bar.s_full);
-        }
-        __syncwarp();
-        ok = guard.wait(bar.full + (n + 1) % S::kSlots, (n + 1) / S::kSlots & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          mma_rows_rows<D>(tP, own + kTile16, ring + (n + 1) % S::kSlots * kTile16);  // dP^T = V dO^T
-          tc::mma_commit(bar.dp_full);
-        }
-        __syncwarp();
-        for (long long j = x.i0; j < x.i1; ++j, n += 2, ++steps) {
-          const uint32_t qs = n % S::kSlots, gs = (n + 1) % S::kSlots;
-          const bool last = j + 1 == x.i1;
-          ok = guard.wait(bar.p_ready, steps & 1) &&
-               (last || guard.wait(bar.full + (n + 2) % S::kSlots, (n + 2) / S::kSlots & 1));
+        uint32_t more = 0;
+        for (int left = (int)(x.i1 - x.i0); left > 0 && ok; --left, ++steps) {
+          ok = second ? guard.wait(bar.a_full + ta.slot, ta.phase) : guard.wait(bar.b_full + tb.slot, tb.phase);
           if (!ok) break;
-          tc::tc_fence_after();
-          if (lane == 0) {
-            mma_tmem_cols<D>(tV, tS, ring_mn + gs * kTile16, j > x.i0);  // dV += P^T dO
-            tc::mma_commit(bar.empty + gs);
-            if (!last) {
-              mma_rows_rows<D>(tS, own, ring + (n + 2) % S::kSlots * kTile16);
-              tc::mma_commit(bar.s_full);
-            }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = guard.wait((second ? bar.ds_ready : bar.p_ready) + half, steps & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (!second)  // dV += P^T dO
+              mma_tmem_cols<D>(tV, tS + half * 64, ring_b_mn + tb.slot * kTile16 + half * kHalf16, more);
+            else  // dK += dS^T Q
+              mma_tmem_cols<D>(tK, tP + half * 64, ring_a_mn + ta.slot * kTile16 + half * kHalf16, more);
+            more = 1;
+            if (left > 1) ok = form(half);
+            if (!ok) break;
           }
-          __syncwarp();
-          ok = guard.wait(bar.ds_ready, steps & 1) &&
-               (last || guard.wait(bar.full + (n + 3) % S::kSlots, (n + 3) / S::kSlots & 1));
           if (!ok) break;
-          tc::tc_fence_after();
-          if (lane == 0) {
-            mma_tmem_cols<D>(tK, tP, ring_mn + qs * kTile16, j > x.i0);  // dK += dS^T Q
-            tc::mma_commit(bar.empty + qs);
-            if (!last) {
-              mma_rows_rows<D>(tP, own + kTile16, ring + (n + 3) % S::kSlots * kTile16);
-              tc::mma_commit(bar.dp_full);
-            } else {
-              tc::mma_commit(bar.done);
-            }
+          if (!second) {
+            tc::mma_commit(bar.b_empty + tb.slot);
+            tb.step();
+          } else {
+            tc::mma_commit(bar.a_empty + ta.slot);
+            ta.step();
           }
-          __syncwarp();
+          if (left == 1) tc::mma_commit(bar.done);
         }
       }
-      if (lane == 0) tc::mma_commit(bar.drain);
-      __syncwarp();
-      tc::mbar_wait(bar.drain, 0, 1000000ull);
+      uint64_t* drain = bar.drain + second;
+      tc::mma_commit(drain);
+      tc::mbar_wait(drain, 0, 1000000ull);
     }
   } else {
     tc::regs_take<kWorkRegs>();
@@ -354,20 +415,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       const bool live = key_seen(a, x.kb, key, x.count);
       for (long long j = x.i0; j < x.i1; ++j, ++steps) {
         const float* rows = sRows + (steps & 1) * 256 + half * 64;
-        ok = guard.wait(bar.rows_full + (steps & 1), steps >> 1 & 1) && guard.wait(bar.s_full, steps & 1);
+        ok = guard.wait(bar.rows_full + (steps & 1), steps >> 1 & 1) && guard.wait(bar.s_full + half, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
         float2 p[32];
+        uint32_t r[64];
+        tc::tmem_ld32(tS + lane_off + half * 64, r);
+        tc::tmem_ld32(tS + lane_off + half * 64 + 32, r + 32);
+        tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t r[32], w[16];
+          uint32_t w[16];
           float nl[32];
-          tc::tmem_ld32(tS + lane_off + half * 64 + c * 32, r);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(nl + e) = *reinterpret_cast<const float4*>(rows + c * 32 + e);
-          tc::tmem_wait_ld();
-          exp_chunk<true>(r, c2, nl, c2, p + c * 16);
+          exp_chunk<true>(r + c * 32, c2, nl, c2, p + c * 16);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             if (!live) p[c * 16 + e] = fm::f2(0.f, 0.f);  // whatever stands in the key's row
@@ -378,22 +441,24 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar.p_ready);
-        ok = guard.wait(bar.dp_full, steps & 1);
+        if (lane == 0) tc::mbar_arrive(bar.p_ready + half);
+        ok = guard.wait(bar.dp_full + half, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
+        tc::tmem_ld32(tP + lane_off + half * 64, r);
+        tc::tmem_ld32(tP + lane_off + half * 64 + 32, r + 32);
+        tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t r[32], w[16];
+          uint32_t w[16];
           float nd[32];
-          tc::tmem_ld32(tP + lane_off + half * 64 + c * 32, r);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(nd + e) = *reinterpret_cast<const float4*>(rows + 128 + c * 32 + e);
-          tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 d = fm::add2(fm::f2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])),
+            const int k = c * 32 + 2 * e;
+            float2 d = fm::add2(fm::f2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
                                 fm::f2(nd[2 * e], nd[2 * e + 1]));
             d = fm::mul2(d, p[c * 16 + e]);
             w[e] = live ? pack_bf16x2(d.x, d.y) : 0u;
@@ -404,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          tc::mbar_arrive(bar.ds_ready);
+          tc::mbar_arrive(bar.ds_ready + half);
           tc::mbar_arrive(bar.rows_empty + (steps & 1));
         }
       }
@@ -481,14 +546,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
                                                                  const CrossArgs a, unsigned int* err, int items,
                                                                  int rtiles) {
   using S = Smem<D>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (tc::smem_u32(sm) & 1023u) {  // no room is left to align it here
+    if (threadIdx.x == 0) atomicOr(err, kErrInternal);
+    return;
+  }
   const Bars bar = bars_of<D>(sm);
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    init_bars<D>(bar);
+    init_bars<D>(bar, 1, kWorkWarps, 1);
     *sAbort = 0;
   }
   if (warp == kMmaWarp) {
@@ -506,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
     tc::regs_give<kOtherRegs>();
     if (warp == kLoadWarp) {
       if (lane == 0) {
-        uint32_t n = 0, own = 0;
+        Turn<S::kSlotsA> ta;
+        Turn<S::kSlotsB> tb;
+        uint32_t na = 0, nb = 0, own = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
           const RowItem x = row_item(a, i, rtiles);
@@ -517,82 +587,101 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
           load_tile<D>(sm + S::kOwn, &maps.q, a.qs, x.row0, x.h, x.b, bar.own_full);
           load_tile<D>(sm + S::kOwn + S::kTileBytes, &maps.g, a.gs, x.row0, x.h, x.b, bar.own_full);
           ++own;
-          for (int j = 2 * x.t0; j < 2 * x.t1; ++j, ++n) {  // K, then V of each tile
-            const int slot = n % S::kSlots;
-            ok = guard.wait(bar.empty + slot, (n / S::kSlots & 1) ^ 1);
+          for (int j = x.t0; j < x.t1; ++j) {
+            ok = guard.wait(bar.a_empty + ta.slot, ta.phase ^ 1);
             if (!ok) break;
-            tc::mbar_arrive_expect_tx(bar.full + slot, S::kTileBytes);
-            const bool v = j & 1;
-            load_tile<D>(sm + S::kRing + slot * S::kTileBytes, v ? &maps.v : &maps.k, v ? a.vs : a.ks, (j >> 1) * 128,
-                         x.kh, x.kb, bar.full + slot);
+            tc::mbar_arrive_expect_tx(bar.a_full + ta.slot, S::kTileBytes);
+            load_tile<D>(sm + S::kRingA + ta.slot * S::kTileBytes, &maps.k, a.ks, j * 128, x.kh, x.kb,
+                         bar.a_full + ta.slot);
+            ta.step();
+            ++na;
+            ok = guard.wait(bar.b_empty + tb.slot, tb.phase ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(bar.b_full + tb.slot, S::kTileBytes);
+            load_tile<D>(sm + S::kRingB + tb.slot * S::kTileBytes, &maps.v, a.vs, j * 128, x.kh, x.kb,
+                         bar.b_full + tb.slot);
+            tb.step();
+            ++nb;
           }
         }
-        for (uint32_t k = n > S::kSlots ? n - S::kSlots : 0; k < n; ++k)
-          tc::mbar_wait(bar.full + k % S::kSlots, k / S::kSlots & 1, 1000000ull);
+        drain_ring(bar.a_full, ta, na);
+        drain_ring(bar.b_full, tb, nb);
         if (own > 0) tc::mbar_wait(bar.own_full, (own - 1) & 1, 1000000ull);
       }
-    } else if (warp == kMmaWarp) {
-      const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
-      const uint64_t ring = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 16, 1024);
-      const uint64_t ring_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRing), 128 * 128, 1024);
-      constexpr int kTile16 = S::kTileBytes >> 4;
-      uint32_t n = 0, own_n = 0, steps = 0;
+    } else if (warp == kHelpWarp) {
+      // K's rows of keys that are left out become zeros: K is a factor of dS K too
+      Turn<S::kSlotsA> ta;
       bool ok = true;
-      // S of the step whose K is the n-th tile of the ring: Q K^T, the keys that
-      // are left out cleared first, since K is a factor of dS K too
-      auto score = [&](const RowItem& x, int j, uint32_t at, uint32_t step) {
-        const uint32_t slot = at % S::kSlots;
-        if (!guard.wait(bar.full + slot, at / S::kSlots & 1)) return false;
-        if (!tile_full(a, j * 128, x.count))  // rows past the tensor's end came as zeros
-          clear_rows<D>(sm + S::kRing + slot * S::kTileBytes, key_bits(a, x.kb, j * 128, x.count, lane),
-                        min(128, a.Nk - j * 128), lane);
-        if (lane == 0) {
-          mma_rows_rows<D>(tmem + (step & 1) * 128, own, ring + slot * kTile16);
-          tc::mma_commit(bar.s_full + (step & 1));
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        const RowItem x = row_item(a, i, rtiles);
+        for (int j = x.t0; j < x.t1; ++j, ta.step()) {
+          ok = guard.wait(bar.a_full + ta.slot, ta.phase);
+          if (!ok) break;
+          if (!tile_full(a, j * 128, x.count))  // rows past the tensor's end came as zeros
+            clear_rows<D>(sm + S::kRingA + ta.slot * S::kTileBytes, key_bits(a, x.kb, j * 128, x.count, lane),
+                          min(128, a.Nk - j * 128), lane);
+          if (lane == 0) tc::mbar_arrive(bar.a_ready + ta.slot);
         }
-        __syncwarp();
+      }
+    } else if (lane == 0) {
+      const bool second = warp > kMmaWarp;  // the chain of dP
+      const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
+      const uint64_t ring_a = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingA), 16, 1024);
+      const uint64_t ring_b = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingB), 16, 1024);
+      const uint64_t ring_a_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingA), 128 * 128, 1024);
+      constexpr int kTile16 = S::kTileBytes >> 4;
+      Turn<S::kSlotsA> ta;
+      Turn<S::kSlotsB> tb;
+      uint32_t own_n = 0, steps = 0;
+      bool ok = true;
+      auto gradient = [&] {  // dP = dO V^T
+        if (!guard.wait(bar.b_full + tb.slot, tb.phase)) return false;
+        mma_rows_rows<D, 128>(tP, own + kTile16, ring_b + tb.slot * kTile16);
+        tc::mma_commit(bar.dp_full);
+        tc::mma_commit(bar.b_empty + tb.slot);
+        tb.step();
         return true;
       };
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const RowItem x = row_item(a, i, rtiles);
         if (x.t0 >= x.t1) continue;
-        ok = guard.wait(bar.own_full, own_n & 1) && score(x, x.t0, n, steps) &&
-             guard.wait(bar.full + (n + 1) % S::kSlots, (n + 1) / S::kSlots & 1);
+        ok = guard.wait(bar.own_full, own_n & 1);
         if (!ok) break;
         ++own_n;
-        if (lane == 0) {
-          mma_rows_rows<D>(tP, own + kTile16, ring + (n + 1) % S::kSlots * kTile16);  // dP = dO V^T
-          tc::mma_commit(bar.dp_full);
-          tc::mma_commit(bar.empty + (n + 1) % S::kSlots);
-        }
-        __syncwarp();
-        for (int j = x.t0; j < x.t1; ++j, n += 2, ++steps) {
-          const uint32_t ks = n % S::kSlots;
-          const bool last = j + 1 == x.t1;
-          // S of the next step into the other half, which dS of the step before
-          // this one was formed from
-          ok = (last || score(x, j + 1, n + 2, steps + 1)) && guard.wait(bar.ds_ready, steps & 1) &&
-               (last || guard.wait(bar.full + (n + 3) % S::kSlots, (n + 3) / S::kSlots & 1));
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (lane == 0) {
-            mma_tmem_cols<D>(tQ, tP, ring_mn + ks * kTile16, j > x.t0);  // dQ += dS K
-            tc::mma_commit(bar.empty + ks);
-            if (!last) {
-              const uint32_t vs = (n + 3) % S::kSlots;
-              mma_rows_rows<D>(tP, own + kTile16, ring + vs * kTile16);
-              tc::mma_commit(bar.dp_full);
-              tc::mma_commit(bar.empty + vs);
-            } else {
-              tc::mma_commit(bar.done);
+        if (second) {
+          ok = gradient();
+          uint32_t more = 0;
+          for (int left = x.t1 - x.t0; left > 0 && ok; --left, ++steps) {
+            ok = guard.wait(bar.a_ready + ta.slot, ta.phase) && guard.wait(bar.ds_ready, steps & 1) &&
+                 guard.wait(bar.ds_ready + 1, steps & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // dQ += dS K
+              mma_tmem_cols<D>(tQ, tP + half * 64, ring_a_mn + ta.slot * kTile16 + half * kHalf16, more);
+              more = 1;
             }
+            tc::mma_commit(bar.a_empty + ta.slot);
+            ta.step();
+            if (left > 1) ok = gradient();
+            else tc::mma_commit(bar.done);
           }
-          __syncwarp();
+        } else {
+          // S of each step in the half of TMEM that the step before the last has left
+          for (int left = x.t1 - x.t0; left > 0; --left, ++steps) {
+            ok = guard.wait(bar.a_ready + ta.slot, ta.phase) &&
+                 guard.wait(bar.p_ready + (steps & 1), (steps >> 1 & 1) ^ 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            mma_rows_rows<D, 128>(tmem + (steps & 1) * 128, own, ring_a + ta.slot * kTile16);
+            tc::mma_commit(bar.s_full + (steps & 1));
+            ta.step();
+          }
         }
       }
-      if (lane == 0) tc::mma_commit(bar.drain);
-      __syncwarp();
-      tc::mbar_wait(bar.drain, 0, 1000000ull);
+      uint64_t* drain = bar.drain + second;
+      tc::mma_commit(drain);
+      tc::mbar_wait(drain, 0, 1000000ull);
     }
   } else {
     tc::regs_take<kWorkRegs>();
@@ -623,24 +712,28 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         if (!ok) break;
         tc::tc_fence_after();
         float2 p[32];
+        uint32_t r[64];
+        tc::tmem_ld32(tmem + (steps & 1) * 128 + lane_off + half * 64, r);
+        tc::tmem_ld32(tmem + (steps & 1) * 128 + lane_off + half * 64 + 32, r + 32);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar.p_ready + (steps & 1));  // S is in registers
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32];
-          tc::tmem_ld32(tmem + (steps & 1) * 128 + lane_off + half * 64 + c * 32, r);
-          tc::tmem_wait_ld();
-          exp_chunk<false>(r, c2, nullptr, nl, p + c * 16);
-        }
+        for (int c = 0; c < 2; ++c) exp_chunk<false>(r + c * 32, c2, nullptr, nl, p + c * 16);
         ok = guard.wait(bar.dp_full, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
+        tc::tmem_ld32(tP + lane_off + half * 64, r);
+        tc::tmem_ld32(tP + lane_off + half * 64 + 32, r + 32);
+        tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t r[32], w[16];
-          tc::tmem_ld32(tP + lane_off + half * 64 + c * 32, r);
-          tc::tmem_wait_ld();
+          uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 d = fm::add2(fm::f2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), nd);
+            const int k = c * 32 + 2 * e;
+            float2 d = fm::add2(fm::f2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), nd);
             d = fm::mul2(d, p[c * 16 + e]);
             if (!whole) {  // P or dP of a key that is left out may be anything
               if (!(bits[c] >> (2 * e) & 1u)) d.x = 0.f;
@@ -653,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar.ds_ready);
+        if (lane == 0) tc::mbar_arrive(bar.ds_ready + half);
       }
       if (!ok) break;
       const bool any = x.t0 < x.t1;
@@ -718,7 +811,7 @@ cudaError_t run_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dV, s, a.Bk, a.Hk, a.Nk, D, 32);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, s, a.Bk, a.Hk, a.Nk, D, 32);
   if (e != cudaSuccess) return e;
-  constexpr int smem = Smem<D>::kTotal + 1024;
+  constexpr int smem = Smem<D>::kTotal;
   e = cudaFuncSetAttribute(cross_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
@@ -735,7 +828,7 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
   if (e != cudaSuccess) return e;
   m.out1 = m.out0;
-  constexpr int smem = Smem<D>::kTotal + 1024;
+  constexpr int smem = Smem<D>::kTotal;
   e = cudaFuncSetAttribute(cross_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int rtiles = (a.Nq + 127) / 128;
