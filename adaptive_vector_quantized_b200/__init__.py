@@ -482,13 +482,13 @@ def avq_gilbert_order(width: int, height: int) -> torch.Tensor:
 
 
 def _view(t, name, shape=None, dtype=None, device=None):
-    """Pointer and strides of a [B,H,N,d] CUDA tensor whose last dimension is
+    """Address and strides of a [B,H,N,d] CUDA tensor whose last dimension is
     contiguous (any view of that kind: heads inside a joint projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, H, N, d], got {tuple(t.shape)}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -496,27 +496,54 @@ def _view(t, name, shape=None, dtype=None, device=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device} (all tensors on one GPU)")
-    if t.stride(3) != 1:
+    b, h, n, d = t.stride()
+    if d != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return _vp(t.data_ptr()), avq_strides(t.stride(0), t.stride(1), t.stride(2))
+    return t.data_ptr(), avq_strides(b, h, n)
 
 
-def _no_view(t):
-    return None, avq_strides(0, 0, 0)
+_NO_VIEW = (None, avq_strides(0, 0, 0))
 
 
-def _launch(dev, stream):
-    """Context in which a call allocates and launches: `dev` current and, when the
-    caller names a stream, that stream current too, so that outputs and
-    workspaces made here come from (and go back to) that stream's memory."""
-    if stream is None:
-        return torch.cuda.device(dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(handle, device=dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, expected {dev}")
-    return torch.cuda.stream(stream)
+def _addr(t):
+    """Address of a contiguous CUDA tensor, None for None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+class _Launch:
+    """Context in which a call allocates and launches, as the raw stream handle:
+    `dev` current and, when the caller names a stream, that stream current too,
+    so that outputs and workspaces made inside come from (and go back to) that
+    stream's memory.  Where both are current already nothing is switched: the
+    smallest calls are bound by the host."""
+    __slots__ = ("inner", "index")
+
+    def __init__(self, dev, stream):
+        self.index = dev.index
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+                stream = torch.cuda.ExternalStream(handle, device=dev)
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, expected {dev}")
+            self.inner = torch.cuda.stream(stream)
+        else:
+            self.inner = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.inner is not None:
+            self.inner.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
 
 
 _NORMS = {"rms": AVQ_NORM_RMS, "layer": AVQ_NORM_LAYER}
@@ -558,12 +585,12 @@ def _qk_dims(Q, K, norm, eps, freqs, positions, layout, mscale, axes):
 def _qk_outputs(Q, K, Yq, Yk):
     _expect(Yq, "the queries' output", Q.shape, Q.dtype, Q.device)
     if Yq is None:
-        Yq = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        Yq = Q.new_empty(Q.shape)
     if K is None:
         return Yq, None
     _expect(Yk, "the keys' output", K.shape, Q.dtype, Q.device)
     if Yk is None:
-        Yk = torch.empty(K.shape, dtype=Q.dtype, device=Q.device)
+        Yk = K.new_empty(K.shape)
     return Yq, Yk
 
 
@@ -593,12 +620,12 @@ def avq_rotary(Q, K=None, freqs=None, positions=None, layout="half", mscale=1.0,
     dims, positions = _qk_dims(Q, K, AVQ_NORM_NONE, 0.0, freqs, positions, layout, mscale, axes)
     dt, dev = _dtype_code(Q), Q.device
     qp, qs = _view(Q, "Q")
-    kp, ks = _no_view(K) if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
-    with _launch(dev, stream):
+    kp, ks = _NO_VIEW if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    with _Launch(dev, stream) as st:
         Yq, Yk = _qk_outputs(Q, K, Yq, Yk)
         _check(lib().avq_rotary(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks),
-                                _ptr(positions), _ptr(freqs), int(bool(inverse)), _ptr(Yq), _ptr(Yk),
-                                _stream(None)))
+                                _addr(positions), _addr(freqs), int(bool(inverse)), _addr(Yq), _addr(Yk),
+                                st))
     return Yq, Yk
 
 
@@ -611,14 +638,14 @@ def avq_qk_norm(Q, K=None, q_weight=None, k_weight=None, q_bias=None, k_bias=Non
     dims, positions = _qk_dims(Q, K, _choice(_NORMS, norm, "norm"), eps, freqs, positions, layout, mscale, axes)
     dt, dev = _dtype_code(Q), Q.device
     qp, qs = _view(Q, "Q")
-    kp, ks = _no_view(K) if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    kp, ks = _NO_VIEW if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (q_bias, "q_bias"), (k_bias, "k_bias")):
         _expect(t, n, (dims.d,), Q.dtype, dev)
-    with _launch(dev, stream):
+    with _Launch(dev, stream) as st:
         Yq, Yk = _qk_outputs(Q, K, Yq, Yk)
-        _check(lib().avq_qk_norm(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks), _ptr(q_weight),
-                                 _ptr(k_weight), _ptr(q_bias), _ptr(k_bias), _ptr(positions), _ptr(freqs), _ptr(Yq),
-                                 _ptr(Yk), _stream(None)))
+        _check(lib().avq_qk_norm(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks), _addr(q_weight),
+                                 _addr(k_weight), _addr(q_bias), _addr(k_bias), _addr(positions), _addr(freqs), _addr(Yq),
+                                 _addr(Yk), st))
     return Yq, Yk
 
 
@@ -633,13 +660,13 @@ def avq_qk_norm_backward(dYq, dYk, Q, K=None, q_weight=None, k_weight=None, norm
         raise ValueError("dYk and K go together")
     dt, dev = _dtype_code(Q), Q.device
     gqp, gqs = _view(dYq, "dYq", Q.shape, Q.dtype, dev)
-    gkp, gks = _no_view(K) if K is None else _view(dYk, "dYk", K.shape, Q.dtype, dev)
+    gkp, gks = _NO_VIEW if K is None else _view(dYk, "dYk", K.shape, Q.dtype, dev)
     qp, qs = _view(Q, "Q")
-    kp, ks = _no_view(K) if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    kp, ks = _NO_VIEW if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         _expect(t, n, (dims.d,), Q.dtype, dev)
     wanted = (q_weight is not None, K is not None and k_weight is not None, bias, bias and K is not None)
-    with _launch(dev, stream):
+    with _Launch(dev, stream) as st:
         dQ, dK = _qk_outputs(Q, K, dQ, dK)
         sums = torch.empty((4, dims.d), dtype=torch.float32, device=dev)
         dwq, dwk, dbq, dbk = (sums[i] if w else None for i, w in enumerate(wanted))
@@ -648,9 +675,9 @@ def avq_qk_norm_backward(dYq, dYk, Q, K=None, q_weight=None, k_weight=None, norm
             ws = torch.empty(n + 256, dtype=torch.uint8, device=dev)
         wp, wn = _ws_ptr(ws, dev)
         _check(lib().avq_qk_norm_backward(ctypes.byref(dims), dt, gqp, ctypes.byref(gqs), gkp, ctypes.byref(gks), qp,
-                                          ctypes.byref(qs), kp, ctypes.byref(ks), _ptr(q_weight), _ptr(k_weight),
-                                          _ptr(positions), _ptr(freqs), _ptr(dQ), _ptr(dK), _ptr(dwq), _ptr(dwk),
-                                          _ptr(dbq), _ptr(dbk), wp, wn, _stream(None)))
+                                          ctypes.byref(qs), kp, ctypes.byref(ks), _addr(q_weight), _addr(k_weight),
+                                          _addr(positions), _addr(freqs), _addr(dQ), _addr(dK), _addr(dwq), _addr(dwk),
+                                          _addr(dbq), _addr(dbk), wp, wn, st))
     return dQ, dK, dwq, dwk, dbq, dbk
 
 
@@ -696,9 +723,9 @@ def avq_cross_attention(Q, K, V, kv_lens=None, key_mask=None, scale=None, O=None
     tensor is written in place."""
     dims, ((qp, qs), (kp, ks), (vp, vs)) = _cross_dims(Q, K, V, kv_lens, key_mask, scale)
     dt, dev = _dtype_code(Q), Q.device
-    with _launch(dev, stream):
+    with _Launch(dev, stream) as st:
         if O is None:
-            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+            O = Q.new_empty(Q.shape)
         op, os_ = _view(O, "O", Q.shape, Q.dtype, dev)
         if isinstance(lse, torch.Tensor):
             _expect(lse, "lse", Q.shape[:3], torch.float32, dev)
@@ -706,8 +733,8 @@ def avq_cross_attention(Q, K, V, kv_lens=None, key_mask=None, scale=None, O=None
             lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=dev) if lse else None
         ws, wp, wn = _cross_ws(dims, dt, False, ws, dev)
         _check(lib().avq_cross_attention(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks), vp,
-                                         ctypes.byref(vs), _ptr(kv_lens), _ptr(key_mask), op, ctypes.byref(os_),
-                                         _ptr(lse), wp, wn, _stream(None)))
+                                         ctypes.byref(vs), _addr(kv_lens), _addr(key_mask), op, ctypes.byref(os_),
+                                         _addr(lse), wp, wn, st))
     return O, lse
 
 
@@ -725,14 +752,14 @@ def avq_cross_attention_backward(dO, Q, K, V, O, lse, kv_lens=None, key_mask=Non
     _expect(lse, "lse", Q.shape[:3], torch.float32, dev)
     for t, name, like in ((dQ, "dQ", Q), (dK, "dK", K), (dV, "dV", K)):
         _expect(t, name, like.shape, Q.dtype, dev)
-    with _launch(dev, stream):
-        dQ, dK, dV = (torch.empty(like.shape, dtype=Q.dtype, device=dev) if t is None else t
+    with _Launch(dev, stream) as st:
+        dQ, dK, dV = (like.new_empty(like.shape) if t is None else t
                       for t, like in ((dQ, Q), (dK, K), (dV, K)))
         ws, wp, wn = _cross_ws(dims, dt, True, ws, dev)
         _check(lib().avq_cross_attention_backward(
             ctypes.byref(dims), dt, gp, ctypes.byref(gs), qp, ctypes.byref(qs), kp, ctypes.byref(ks), vp,
-            ctypes.byref(vs), op, ctypes.byref(os_), _ptr(lse), _ptr(kv_lens), _ptr(key_mask), _ptr(dQ), _ptr(dK),
-            _ptr(dV), wp, wn, _stream(None)))
+            ctypes.byref(vs), op, ctypes.byref(os_), _addr(lse), _addr(kv_lens), _addr(key_mask), _addr(dQ), _addr(dK),
+            _addr(dV), wp, wn, st))
     return dQ, dK, dV
 
 

@@ -2,6 +2,8 @@
 // of the forward pass, the gradients and the joins share.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc_util.cuh"
@@ -20,6 +22,21 @@ __device__ __forceinline__ int key_count(const CrossArgs& a, int kb) {
 }
 __device__ __forceinline__ bool key_seen(const CrossArgs& a, int kb, int j, int count) {
   return j < count && (a.key_mask == nullptr || __ldg(a.key_mask + (size_t)kb * a.Nk + j) != 0);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory: asked of the runtime once
+// per kernel and device, since small calls are bound by the host.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 template <typename T>

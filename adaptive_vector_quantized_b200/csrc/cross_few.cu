@@ -325,7 +325,7 @@ cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e == cudaSuccess) e = make_tmap_view_bf16(&v, a.V, a.vs, a.Bk, a.Hk, a.Nk, D, kTile);
   if (e != cudaSuccess) return e;
   constexpr int smem = Smem<D, ROWS>::kTotal + 1024;
-  e = cudaFuncSetAttribute(cross_few_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_smem<cross_few_kernel<D, ROWS>>(smem);
   if (e != cudaSuccess) return e;
   const int items = a.Bk * a.Hk * chunks * a.splits;
   const int grid = items < 2 * num_sms() ? items : 2 * num_sms();

@@ -379,15 +379,10 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dq_kernel(const CrossArgs
   }
 }
 
-template <typename F>
-cudaError_t with_smem(F* kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <typename T, int D>
 cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(3 * kT * pitch<D>() + kT * kPS) * sizeof(float);
-  cudaError_t e = with_smem(cross_simt_kernel<T, D>, smem);
+  cudaError_t e = allow_smem<cross_simt_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
   cross_simt_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
@@ -396,7 +391,7 @@ cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(4 * kT * pitch<D>() + 2 * kT * kPS) * sizeof(float);
-  cudaError_t e = with_smem(cross_simt_dkv_kernel<T, D>, smem);
+  cudaError_t e = allow_smem<cross_simt_dkv_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT)), a.splits);
   cross_simt_dkv_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
@@ -405,7 +400,7 @@ cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(4 * kT * pitch<D>() + kT * kPS) * sizeof(float);
-  cudaError_t e = with_smem(cross_simt_dq_kernel<T, D>, smem);
+  cudaError_t e = allow_smem<cross_simt_dq_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
   cross_simt_dq_kernel<T, D><<<grid, kThreads, smem, st>>>(a);

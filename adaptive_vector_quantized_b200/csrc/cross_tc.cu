@@ -522,7 +522,7 @@ cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.o, a.O, a.os, a.B, a.Hq, a.Nq, D, 32);
   if (e != cudaSuccess) return e;
   constexpr int smem = Smem<D>::kTotal + 1024;
-  e = cudaFuncSetAttribute(cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_smem<cross_tc_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int pairs = (a.Nq + 2 * kRowTile - 1) / (2 * kRowTile);
   const long long items = (long long)a.B * a.Hq * pairs * a.splits;

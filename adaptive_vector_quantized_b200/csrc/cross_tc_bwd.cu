@@ -812,7 +812,7 @@ cudaError_t run_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, s, a.Bk, a.Hk, a.Nk, D, 32);
   if (e != cudaSuccess) return e;
   constexpr int smem = Smem<D>::kTotal;
-  e = cudaFuncSetAttribute(cross_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_smem<cross_tc_dkv_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
   const long long items = (long long)a.Bk * a.Hk * ktiles * a.splits;
@@ -829,7 +829,7 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   m.out1 = m.out0;
   constexpr int smem = Smem<D>::kTotal;
-  e = cudaFuncSetAttribute(cross_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_smem<cross_tc_dq_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int rtiles = (a.Nq + 127) / 128;
   const long long items = (long long)a.B * a.Hq * rtiles * a.splits;
