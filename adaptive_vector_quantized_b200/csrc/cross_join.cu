@@ -39,6 +39,47 @@ __global__ void __launch_bounds__(kThreads) cross_join_kernel(const CrossArgs a)
   if (c == 0 && a.lse != nullptr) a.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
+// The same for items whose partial results lie together: [item][split][row], and
+// for dQ, which is a plain sum.  One row per d / 4 lanes.
+template <int D, bool kSoftmax>
+__global__ void __launch_bounds__(kThreads) cross_join_items_kernel(const CrossArgs a, int per_head, int rows,
+                                                                    long long total) {
+  grid_dependency_wait();
+  constexpr int L = D / 4;
+  const long long g = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  if (g >= total) return;
+  const int c = (threadIdx.x % L) * 4;
+  const int j = (int)(g / rows), r = (int)(g % rows);
+  const int item = a.whole + j, bh = item / per_head;
+  const int n = item % per_head * rows + r, h = bh % a.Hq, b = bh / a.Hq;
+  if (n >= a.Nq) return;
+  const size_t first = (size_t)j * a.splits * rows + r;
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f, m = -INFINITY;
+  if constexpr (kSoftmax)
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_lse[first + (size_t)s * rows]);
+  for (int s = 0; s < a.splits; ++s) {
+    float w = 1.f;
+    if constexpr (kSoftmax) {
+      const float l = a.part_lse[first + (size_t)s * rows];
+      if (l == -INFINITY) continue;
+      w = exp2f((l - m) * kLog2e);
+      z += w;
+    }
+    const float4 v = *reinterpret_cast<const float4*>(a.part + (first + (size_t)s * rows) * D + c);
+    o[0] += w * v.x, o[1] += w * v.y, o[2] += w * v.z, o[3] += w * v.w;
+  }
+  const size_t row = ((size_t)b * a.Hq + h) * a.Nq + n;
+  if constexpr (kSoftmax) {
+    const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= inv;
+    put4(static_cast<bf16*>(a.O) + b * a.os.b + h * a.os.h + n * a.os.n + c, o);
+    if (c == 0 && a.lse != nullptr) a.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+  } else {
+    put4(static_cast<bf16*>(a.dQ) + row * D + c, o);
+  }
+}
+
 // out[i] = sum_s part[s * stride + i], in the order of s
 template <typename T>
 __global__ void __launch_bounds__(kThreads) partial_sum_kernel(const float* part, size_t stride, int splits, T* out,
@@ -98,6 +139,19 @@ cudaError_t launch_cross_join(const CrossArgs& a, avq_dtype dt, cudaStream_t st,
                      : launch_after(cross_join_kernel<float, 128>, grid, dim3(kThreads), 0, st, a);
   return a.d == 64 ? launch_after(cross_join_kernel<bf16, 64>, grid, dim3(kThreads), 0, st, a)
                    : launch_after(cross_join_kernel<bf16, 128>, grid, dim3(kThreads), 0, st, a);
+}
+
+cudaError_t launch_cross_join_items(const CrossArgs& a, int items, int per_head, int rows, bool softmax,
+                                    cudaStream_t st, LaunchLog& log) {
+  const long long total = (long long)(items - a.whole) * rows;
+  const int per = kThreads / (a.d / 4);
+  const dim3 grid((unsigned)((total + per - 1) / per));
+  log.add("cross_join");
+  if (a.d == 64)
+    return softmax ? launch_after(cross_join_items_kernel<64, true>, grid, dim3(kThreads), 0, st, a, per_head, rows, total)
+                   : launch_after(cross_join_items_kernel<64, false>, grid, dim3(kThreads), 0, st, a, per_head, rows, total);
+  return softmax ? launch_after(cross_join_items_kernel<128, true>, grid, dim3(kThreads), 0, st, a, per_head, rows, total)
+                 : launch_after(cross_join_items_kernel<128, false>, grid, dim3(kThreads), 0, st, a, per_head, rows, total);
 }
 
 cudaError_t launch_partial_sum(avq_dtype dt, const float* part, size_t stride, int splits, void* out, size_t n,

@@ -66,14 +66,14 @@ constexpr int kStep = 64;  // keys of a softmax step: half a key tile
 
 // One item: a pair of row tiles of a head and a range of key tiles.
 struct Item {
-  int b, h, kb, kh, row0, tiles, count, t0, t1, split;
+  int b, h, kb, kh, row0, tiles, count, t0, t1, parts;
 };
 
 __device__ __forceinline__ Item item_of(const CrossArgs& a, int i, int pairs) {
   Item x;
-  const int pair = i % pairs, rest = i / pairs;
-  x.split = rest % a.splits;
-  const int bh = rest / a.splits;
+  const Part part = part_of(a, i);
+  x.parts = part.parts;
+  const int pair = part.item % pairs, bh = part.item / pairs;
   x.b = bh / a.Hq;
   x.h = bh % a.Hq;
   x.kb = x.b / (a.B / a.Bk);
@@ -82,8 +82,8 @@ __device__ __forceinline__ Item item_of(const CrossArgs& a, int i, int pairs) {
   x.tiles = x.row0 + kRowTile < a.Nq ? 2 : 1;
   x.count = key_count(a, x.kb);
   const int kt = (x.count + kKeyTile - 1) / kKeyTile;
-  x.t0 = (int)((long long)kt * x.split / a.splits);
-  x.t1 = (int)((long long)kt * (x.split + 1) / a.splits);
+  x.t0 = (int)((long long)kt * part.split / part.parts);
+  x.t1 = (int)((long long)kt * (part.split + 1) / part.parts);
   return x;
 }
 
@@ -446,13 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         o_phase ^= 1;
         tc::tc_fence_after();
       }
+      const size_t prow = (size_t)(i - a.whole) * (2 * kRowTile) + t * kRowTile + row;  // of a partial result
       if (live) {
-        if (a.splits > 1) a.part_lse[(size_t)x.split * a.B * a.Hq * a.Nq + grow] = lse;
+        if (x.parts > 1) a.part_lse[prow] = lse;
         else if (a.lse != nullptr) a.lse[grow] = lse;
       }
-      if (a.splits > 1) {
+      if (x.parts > 1) {
         // partial results stay in fp32: a row to a thread, straight to memory
-        float* dst = a.part + ((size_t)x.split * a.B * a.Hq * a.Nq + grow) * D;
+        float* dst = a.part + prow * D;
         if (any) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
 }
 
 template <int D>
-cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
+cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   Maps m;
   cudaError_t e = make_tmap_view_bf16(&m.q, a.Q, a.qs, a.B, a.Hq, a.Nq, D, kRowTile);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.k, a.K, a.ks, a.Bk, a.Hk, a.Nk, D, kKeyTile);
@@ -525,17 +526,20 @@ cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   e = allow_smem<cross_tc_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int pairs = (a.Nq + 2 * kRowTile - 1) / (2 * kRowTile);
-  const long long items = (long long)a.B * a.Hq * pairs * a.splits;
-  const int grid = (int)(items < num_sms() ? items : num_sms());
-  cross_tc_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, (int)items, pairs);
-  return cudaGetLastError();
+  const int items = a.B * a.Hq * pairs;
+  const int launch = a.whole + (items - a.whole) * a.splits;
+  const int grid = launch < num_sms() ? launch : num_sms();
+  cross_tc_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, launch, pairs);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && a.whole < items) e = launch_cross_join_items(a, items, pairs, 2 * kRowTile, true, st, log);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t launch_cross_tc(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   log.add("cross_tc");
-  return a.d == 64 ? run<64>(a, err, st) : run<128>(a, err, st);
+  return a.d == 64 ? run<64>(a, err, st, log) : run<128>(a, err, st, log);
 }
 
 }  // namespace avq

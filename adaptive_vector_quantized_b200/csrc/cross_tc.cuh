@@ -38,6 +38,17 @@ __device__ __forceinline__ bool wait_all(const Guard& g, uint64_t* bar, uint32_t
 // A value that every lane holds, known to the compiler as such.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// Launch item i of a kernel that owns rows: the item of the problem, which of
+// its parts, and of how many.
+struct Part {
+  int item, split, parts;
+};
+__device__ __forceinline__ Part part_of(const CrossArgs& a, int i) {
+  if (i < a.whole) return Part{i, 0, 1};
+  const int j = i - a.whole;
+  return Part{a.whole + j / a.splits, j % a.splits, a.splits};
+}
+
 // Bit i of word w: key k0 + 32 w + i is looked at.  All lanes get all words.
 struct KeyBits {
   uint32_t w[4];

@@ -522,22 +522,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
 // ---- dQ ------------------------------------------------------------------------------
 
 struct RowItem {
-  int b, h, kb, kh, row0, count, t0, t1, split;
+  int b, h, kb, kh, row0, count, t0, t1, parts;
 };
 __device__ __forceinline__ RowItem row_item(const CrossArgs& a, int i, int rtiles) {
   RowItem x;
-  x.row0 = i % rtiles * 128;
-  const int rest = i / rtiles;
-  x.split = rest % a.splits;
-  const int bh = rest / a.splits;
+  const Part part = part_of(a, i);
+  x.parts = part.parts;
+  x.row0 = part.item % rtiles * 128;
+  const int bh = part.item / rtiles;
   x.b = bh / a.Hq;
   x.h = bh % a.Hq;
   x.kb = x.b / (a.B / a.Bk);
   x.kh = x.h / (a.Hq / a.Hk);
   x.count = key_count(a, x.kb);
   const int kt = (x.count + 127) / 128;
-  x.t0 = (int)((long long)kt * x.split / a.splits);
-  x.t1 = (int)((long long)kt * (x.split + 1) / a.splits);
+  x.t0 = (int)((long long)kt * part.split / part.parts);
+  x.t1 = (int)((long long)kt * (part.split + 1) / part.parts);
   return x;
 }
 
@@ -758,8 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
       }
       // 64 columns of dQ to a group
       if (half < S::kBlocks) {
-        if (a.splits > 1) {
-          float* dst = a.part + ((size_t)x.split * a.B * a.Hq * a.Nq + at) * D + half * 64;
+        if (x.parts > 1) {
+          float* dst = a.part + ((size_t)(i - a.whole) * 128 + quarter * 32 + lane) * D + half * 64;
           if (any) {
             store_partial<64>(tQ + lane_off + half * 64, a.scale, dst, in);
           } else if (in) {
@@ -822,7 +822,7 @@ cudaError_t run_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
+cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   Maps m;
   cudaError_t e = maps_of<D>(a, &m);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
@@ -832,10 +832,13 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   e = allow_smem<cross_tc_dq_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
   const int rtiles = (a.Nq + 127) / 128;
-  const long long items = (long long)a.B * a.Hq * rtiles * a.splits;
-  const int grid = (int)(items < num_sms() ? items : num_sms());
-  cross_tc_dq_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, (int)items, rtiles);
-  return cudaGetLastError();
+  const int items = a.B * a.Hq * rtiles;
+  const int launch = a.whole + (items - a.whole) * a.splits;
+  const int grid = launch < num_sms() ? launch : num_sms();
+  cross_tc_dq_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, launch, rtiles);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && a.whole < items) e = launch_cross_join_items(a, items, rtiles, 128, false, st, log);
+  return e;
 }
 
 }  // namespace
@@ -846,7 +849,7 @@ cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStrea
 }
 cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   log.add("cross_tc_dq");
-  return a.d == 64 ? run_dq<64>(a, err, st) : run_dq<128>(a, err, st);
+  return a.d == 64 ? run_dq<64>(a, err, st, log) : run_dq<128>(a, err, st, log);
 }
 
 }  // namespace avq

@@ -172,11 +172,37 @@ long long tiles64(long long n) { return (n + 63) / 64; }
 // Rows per key head up to which the keys are streamed through registers.
 constexpr long long kFewRows = 32;
 
+// How the items of a kernel with one block per SM, each a walk over `units` key
+// tiles, fill its rounds: the items of full rounds stay whole, those of the last
+// round are split where two or more parts of at least four tiles each fit it.
+// 64 pairs of row tiles of each of 8 heads of 128 over 16384 keys (3.46 rounds): 990
+// us whole, 895 us with the last round split in two.
+struct Rounds {
+  int whole = 0, splits = 1;
+  long long parts = 0;  // partial results
+};
+Rounds rounds_of(long long items, long long units) {
+  Rounds r;
+  const long long sms = num_sms(), rest = items % sms;
+  long long n = rest > 0 ? sms / rest : 1;
+  if (n > units / 4) n = units / 4;
+  if (n > 64) n = 64;
+  if (n < 2) {
+    r.whole = (int)items;
+    return r;
+  }
+  r.whole = (int)(items - rest);
+  r.splits = (int)n;
+  r.parts = rest * n;
+  return r;
+}
+
 // How a call is carried out, from its sizes, type and path alone.
 struct CrossPlan {
   bool tc = false;   // tensor-core kernels
   bool few = false;  // the one for few rows per key head
-  int splits = 1;   // forward
+  int splits = 1;    // forward, except for tc
+  Rounds rounds;     // tc: forward, or dQ
   int dkv_splits = 1, dq_splits = 1;
   size_t part = 0, part_lse = 0, delta = 0;  // bytes, each a multiple of 256
   size_t total() const { return part + part_lse + delta; }
@@ -187,21 +213,21 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   const long long target = 2ll * num_sms();
   const long long rows = (long long)s.B * s.Hq * s.Nq, keys = (long long)s.Bk * s.Hk * s.Nk;
   const long long row_items = (long long)s.B * s.Hq * tiles64(s.Nq), key_items = (long long)s.Bk * s.Hk * tiles64(s.Nk);
-  const long long row_units = (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * tiles64(s.Nq);
+  const long long shared = (long long)(s.B / s.Bk) * (s.Hq / s.Hk);  // query heads that read one key head
+  const long long key_tiles = (s.Nk + 127) / 128;
   p.tc = dt == AVQ_BF16 && api_path() != AVQ_PATH_SIMT && s.Nk > 0;
   if (!backward) {
-    p.splits = split_count(row_items, tiles64(s.Nk), target);
-    const long long shared = (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * s.Nq;  // rows that read one key head
-    p.few = p.tc && shared <= kFewRows;
-    if (p.few) {
-      // two rounds of the resident blocks, since lengths differ: 32 sequences
-      // of 4096 to 8191 keys took 68 us with 1 or 2 rounds, 71 with 4, 78 with 8
-      const long long blocks = (long long)s.Bk * s.Hk * ((shared + 15) / 16);
-      p.splits = split_count(blocks, s.Nk / 128, 4ll * num_sms());
-    } else if (p.tc) {  // one block per SM, pairs of 128-row tiles, 128-key tiles
-      const long long pairs = (long long)s.B * s.Hq * ((s.Nq + 255) / 256);
-      p.splits = split_count(pairs, (s.Nk + 127) / 128, num_sms());
+    p.few = p.tc && shared * s.Nq <= kFewRows;
+    if (p.tc && !p.few) {  // pairs of 128-row tiles
+      p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 255) / 256), key_tiles);
+      p.part = up256((size_t)p.rounds.parts * 256 * s.d * 4);
+      p.part_lse = up256((size_t)p.rounds.parts * 256 * 4);
+      return p;
     }
+    // few: two rounds of the resident blocks, since lengths differ (32 sequences
+    // of 4096 to 8191 keys took 68 us with 1 or 2 rounds, 71 with 4, 78 with 8)
+    p.splits = p.few ? split_count((long long)s.Bk * s.Hk * ((shared * s.Nq + 15) / 16), s.Nk / 128, 4ll * num_sms())
+                     : split_count(row_items, tiles64(s.Nk), target);
     if (p.splits > 1) {
       p.part = up256((size_t)p.splits * rows * s.d * 4);
       p.part_lse = up256((size_t)p.splits * rows * 4);
@@ -209,15 +235,17 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
     return p;
   }
   p.delta = up256((size_t)rows * 4);
-  p.dq_splits = split_count(row_items, tiles64(s.Nk), target);
-  if (key_items > 0) p.dkv_splits = split_count(key_items, row_units, target);
-  if (p.tc) {  // one block per SM, tiles of 128
-    const long long q = (s.Nq + 127) / 128, k = (s.Nk + 127) / 128;
-    p.dq_splits = split_count((long long)s.B * s.Hq * q, k, num_sms());
-    p.dkv_splits = split_count((long long)s.Bk * s.Hk * k, (long long)(s.B / s.Bk) * (s.Hq / s.Hk) * q, num_sms());
-  }
   // dK and dV, then dQ, one after the other in the same place
-  const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * rows * s.d * 4 : 0;
+  size_t dq;
+  if (p.tc) {
+    p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 127) / 128), key_tiles);
+    dq = (size_t)p.rounds.parts * 128 * s.d * 4;
+    p.dkv_splits = split_count((long long)s.Bk * s.Hk * key_tiles, shared * ((s.Nq + 127) / 128), num_sms());
+  } else {
+    p.dq_splits = split_count(row_items, tiles64(s.Nk), target);
+    dq = p.dq_splits > 1 ? (size_t)p.dq_splits * rows * s.d * 4 : 0;
+    if (key_items > 0) p.dkv_splits = split_count(key_items, shared * tiles64(s.Nq), target);
+  }
   const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * keys * s.d * 4 : 0;
   p.part = up256(dq > dkv ? dq : dkv);
   return p;
@@ -367,7 +395,9 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
     return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_cross_attention)");
   a.O = O;
   a.lse = lse;
-  a.splits = p.splits;
+  const bool items = p.tc && !p.few;
+  a.splits = items ? p.rounds.splits : p.splits;
+  a.whole = p.rounds.whole;
   a.part = static_cast<float*>(ws);
   a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -380,7 +410,7 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   } else {
     e = launch_cross_simt(a, dtype, cs, log);
   }
-  if (e == cudaSuccess && a.splits > 1) e = launch_cross_join(a, dtype, cs, log);
+  if (e == cudaSuccess && !items && a.splits > 1) e = launch_cross_join(a, dtype, cs, log);
   return api_finish(e, "cross attention launch", log);
 }
 
@@ -443,9 +473,11 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
     }
   }
   if (e == cudaSuccess) {
-    a.splits = p.dq_splits;
+    a.splits = p.tc ? p.rounds.splits : p.dq_splits;
+    a.whole = p.rounds.whole;
     e = p.tc ? launch_cross_tc_dq(a, err, cs, log) : launch_cross_simt_dq(a, dtype, cs, log);
-    if (e == cudaSuccess && a.splits > 1) e = launch_partial_sum(dtype, a.part, qn, a.splits, dQ, qn, cs, log);
+    if (e == cudaSuccess && p.dq_splits > 1)
+      e = launch_partial_sum(dtype, a.part, qn, p.dq_splits, dQ, qn, cs, log);
   }
   return api_finish(e, "cross attention backward launch", log);
 }

@@ -135,10 +135,12 @@ cudaError_t launch_qk_norm_backward(const avq_qk_dims& s, avq_dtype dt, const vo
 // Everything the cross attention's kernels read and write.  splits: ranges
 // of the long axis (keys, or query rows for dK and dV) whose partial results
 // go to `part` (and `part_lse`) in fp32 and are joined by a launch of their own.
+// whole: in the tensor-core kernels that own rows, the leading items (row
+// tiles, or pairs of them) that are not split.
 struct CrossArgs {
   int B, Bk, Hq, Hk, Nq, Nk, d;
   float scale;
-  int splits;
+  int splits, whole;
   Strides qs, ks, vs, os, gs;
   const void *Q, *K, *V, *G;  // G: the gradient of O
   void *O, *dQ, *dK, *dV;
@@ -151,6 +153,11 @@ cudaError_t launch_cross_simt_dkv(const CrossArgs& a, avq_dtype dt, cudaStream_t
 cudaError_t launch_cross_simt_dq(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
 // Joins the forward pass's partial results (softmaxes over disjoint keys).
 cudaError_t launch_cross_join(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+// Joins the split items of the tensor-core kernels that own rows: a.splits
+// partial results of `rows` rows each for every item from a.whole on; `items` in
+// all, `per_head` of them to a head.  softmax: O and lse, else dQ by sums.
+cudaError_t launch_cross_join_items(const CrossArgs& a, int items, int per_head, int rows, bool softmax,
+                                    cudaStream_t st, LaunchLog& log);
 // out[i] = sum over s < splits of part[s * stride + i], i < n (a multiple of 4).
 cudaError_t launch_partial_sum(avq_dtype dt, const float* part, size_t stride, int splits, void* out, size_t n,
                                cudaStream_t st, LaunchLog& log);
