@@ -80,18 +80,19 @@ __global__ void __launch_bounds__(kThreads) cross_join_items_kernel(const CrossA
   }
 }
 
-// out[i] = sum_s part[s * stride + i], in the order of s
+// out[o][i] = sum_s part[s][o][i], in the order of s; n4: floats of an output / 4.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) partial_sum_kernel(const float* part, size_t stride, int splits, T* out,
+__global__ void __launch_bounds__(kThreads) partial_sum_kernel(const float* part, int splits, T* out0, T* out1,
                                                                size_t n4) {
   grid_dependency_wait();
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (size_t)gridDim.x * kThreads) {
+  const size_t all = out1 != nullptr ? 2 * n4 : n4;
+  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += (size_t)gridDim.x * kThreads) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < splits; ++s) {
-      const float4 x = *reinterpret_cast<const float4*>(part + s * stride + i * 4);
+      const float4 x = *reinterpret_cast<const float4*>(part + (s * all + i) * 4);
       v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
     }
-    put4(out + i * 4, v);
+    put4(i < n4 ? out0 + i * 4 : out1 + (i - n4) * 4, v);
   }
 }
 
@@ -118,13 +119,13 @@ __global__ void __launch_bounds__(kThreads) cross_delta_kernel(const CrossArgs a
 }
 
 template <typename T>
-cudaError_t sum_as(const float* part, size_t stride, int splits, void* out, size_t n, cudaStream_t st) {
+cudaError_t sum_as(const float* part, int splits, void* const* out, int outs, size_t n, cudaStream_t st) {
   const size_t n4 = n / 4;
-  size_t blocks = (n4 + kThreads - 1) / kThreads;
+  size_t blocks = (n4 * outs + kThreads - 1) / kThreads;
   const size_t most = (size_t)num_sms() * 8;
   if (blocks > most) blocks = most;
-  return launch_after(partial_sum_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, part, stride, splits,
-                      static_cast<T*>(out), n4);
+  return launch_after(partial_sum_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, part, splits,
+                      static_cast<T*>(out[0]), outs > 1 ? static_cast<T*>(out[1]) : (T*)nullptr, n4);
 }
 
 }  // namespace
@@ -147,17 +148,17 @@ cudaError_t launch_cross_join_items(const CrossArgs& a, int items, int per_head,
   const int per = kThreads / (a.d / 4);
   const dim3 grid((unsigned)((total + per - 1) / per));
   log.add("cross_join");
-  if (a.d == 64)
-    return softmax ? launch_after(cross_join_items_kernel<64, true>, grid, dim3(kThreads), 0, st, a, per_head, rows, total)
-                   : launch_after(cross_join_items_kernel<64, false>, grid, dim3(kThreads), 0, st, a, per_head, rows, total);
-  return softmax ? launch_after(cross_join_items_kernel<128, true>, grid, dim3(kThreads), 0, st, a, per_head, rows, total)
-                 : launch_after(cross_join_items_kernel<128, false>, grid, dim3(kThreads), 0, st, a, per_head, rows, total);
+  auto run = [&](auto kernel) {
+    return launch_after(kernel, grid, dim3(kThreads), 0, st, a, per_head, rows, total);
+  };
+  if (a.d == 64) return softmax ? run(cross_join_items_kernel<64, true>) : run(cross_join_items_kernel<64, false>);
+  return softmax ? run(cross_join_items_kernel<128, true>) : run(cross_join_items_kernel<128, false>);
 }
 
-cudaError_t launch_partial_sum(avq_dtype dt, const float* part, size_t stride, int splits, void* out, size_t n,
+cudaError_t launch_partial_sum(avq_dtype dt, const float* part, int splits, void* const* out, int outs, size_t n,
                                cudaStream_t st, LaunchLog& log) {
   log.add("partial_sum");
-  return dt == AVQ_F32 ? sum_as<float>(part, stride, splits, out, n, st) : sum_as<bf16>(part, stride, splits, out, n, st);
+  return dt == AVQ_F32 ? sum_as<float>(part, splits, out, outs, n, st) : sum_as<bf16>(part, splits, out, outs, n, st);
 }
 
 cudaError_t launch_cross_delta(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log) {

@@ -22,6 +22,12 @@
 // takes 48 clocks of shared memory reads, one with 128 takes 64.
 #include "cross_tc.cuh"
 
+//
+// With at most one key tile (text states) and d = 64 the dK/dV blocks see every
+// key of a row, and TMEM has room: they form dQ too, from a copy of dS in shared
+// memory (the rows of dS^T are keys, so it is read column by column), and Q and
+// dO are read once: 24 heads of 4096 rows over 77 keys 65 us apart, 39 us so.
+
 namespace avq {
 
 namespace {
@@ -44,17 +50,21 @@ struct Smem {
   static constexpr int kRingA = 2 * kTileBytes;
   static constexpr int kRingB = kRingA + kSlotsA * kTileBytes;
   static constexpr int kRows = kRingB + kSlotsB * kTileBytes;  // [2 stages][lse, delta][128]
-  static constexpr int kBar = kRows + 2 * 1024;
+  // where dK/dV blocks form dQ too: dS [2 halves of the rows][128 keys][64], dQ staged [8 warps][32 rows][64]
+  static constexpr bool kRoom = D == 64;
+  static constexpr int kDS = kRows + 2 * 1024;
+  static constexpr int kOutQ = kDS + (kRoom ? 2 * 16384 : 0);
+  static constexpr int kBar = kOutQ + (kRoom ? kWorkWarps * 4096 : 0);
   // a_full[3], a_empty[3], a_ready[3], b_full[2], b_empty[2], own_full, own_empty, s_full[2], dp_full[2], p_ready[2],
-  // ds_ready[2], done, rows_full[2], rows_empty[2], drain[2]
-  static constexpr int kBars = 3 * kSlotsA + 2 * kSlotsB + 17;
+  // ds_ready[2], done, rows_full[2], rows_empty[2], drain[2], dq_full[2], dq_taken[2], own_ready
+  static constexpr int kBars = 3 * kSlotsA + 2 * kSlotsB + 22;
   static constexpr int kMisc = kBar + kBars * 8;
   static constexpr int kTotal = kMisc + 16;
 };
 
 struct Bars {
   uint64_t *a_full, *a_empty, *a_ready, *b_full, *b_empty, *own_full, *own_empty, *s_full, *dp_full, *p_ready,
-      *ds_ready, *done, *rows_full, *rows_empty, *drain;
+      *ds_ready, *done, *rows_full, *rows_empty, *drain, *dq_full, *dq_taken, *own_ready;
 };
 template <int D>
 __device__ __forceinline__ Bars bars_of(uint8_t* sm) {
@@ -75,6 +85,9 @@ __device__ __forceinline__ Bars bars_of(uint8_t* sm) {
   b.rows_full = b.done + 1;
   b.rows_empty = b.rows_full + 2;
   b.drain = b.rows_empty + 2;
+  b.dq_full = b.drain + 2;
+  b.dq_taken = b.dq_full + 2;
+  b.own_ready = b.dq_taken + 2;
   return b;
 }
 // A ring's slot and phase, stepped along.
@@ -99,7 +112,7 @@ __device__ __forceinline__ void init_bars(const Bars& b, int b_users, int p_warp
     if (x == b.own_empty || (x >= b.rows_empty && x < b.drain)) n = kWorkWarps;
     if (x >= b.b_empty && x < b.own_full) n = b_users;
     if (x >= b.p_ready && x < b.ds_ready) n = p_warps;
-    if (x >= b.ds_ready && x < b.done) n = kWorkWarps / 2;
+    if ((x >= b.ds_ready && x < b.done) || (x >= b.dq_taken && x < b.own_ready)) n = kWorkWarps / 2;
     if (x == b.done) n = done_users;
     tc::mbar_init(x, n);
   }
@@ -115,7 +128,7 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, Turn<kSlots> t, uint3
 }
 
 struct Maps {
-  CUtensorMap q, g, k, v, out0, out1;  // out: dV, dK, or dQ
+  CUtensorMap q, g, k, v, out0, out1, out2;  // out: dV, dK and dQ, or dQ alone
 };
 
 // A [128 rows][D] tile by TMA
@@ -209,7 +222,8 @@ struct KeyItem {
   int kb, kh, k0, count, split;
   long long i0, i1;  // row tiles of the query heads and entries that share the key head
 };
-__device__ __forceinline__ KeyItem key_item(const CrossArgs& a, int i, int ktiles, int rtiles) {
+// any_rows: also of a tile with no key (its rows' dQ are written here).
+__device__ __forceinline__ KeyItem key_item(const CrossArgs& a, int i, int ktiles, int rtiles, bool any_rows = false) {
   KeyItem x;
   x.k0 = i % ktiles * 128;
   const int rest = i / ktiles;
@@ -218,7 +232,7 @@ __device__ __forceinline__ KeyItem key_item(const CrossArgs& a, int i, int ktile
   x.kb = bh / a.Hk;
   x.kh = bh % a.Hk;
   x.count = key_count(a, x.kb);
-  const long long all = x.k0 < x.count ? (long long)(a.B / a.Bk) * (a.Hq / a.Hk) * rtiles : 0;
+  const long long all = any_rows || x.k0 < x.count ? (long long)(a.B / a.Bk) * (a.Hq / a.Hk) * rtiles : 0;
   x.i0 = all * x.split / a.splits;
   x.i1 = all * (x.split + 1) / a.splits;
   return x;
@@ -232,7 +246,7 @@ __device__ __forceinline__ RowTile row_tile(const CrossArgs& a, const KeyItem& x
   return RowTile{x.kb * R + rg / G, x.kh * G + rg % G, (int)(i % rtiles) * 128};
 }
 
-template <int D>
+template <int D, bool kWithQ>
 __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_constant__ Maps maps,
                                                                   const CrossArgs a, unsigned int* err, int items,
                                                                   int ktiles, int rtiles) {
@@ -258,9 +272,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  grid_dependency_wait();  // delta
   const Guard guard{err, sAbort};
   const uint32_t tmem = *sTmem;
-  const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 256 + D;  // S | dP | dV | dK
+  // S | dP | dV | dK, and behind them dQ of even and of odd steps
+  const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 256 + D, tQ = tmem + 256 + 2 * D;
 
   if (warp >= kWorkWarps) {
     tc::regs_give<kOtherRegs>();
@@ -302,10 +318,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         if (own > 0) tc::mbar_wait(bar.own_full, (own - 1) & 1, 1000000ull);
       }
     } else if (warp == kHelpWarp) {
-      uint32_t n = 0;
+      uint32_t n = 0, own = 0;
       bool ok = true;
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const KeyItem x = key_item(a, i, ktiles, rtiles);
+        if (kWithQ && x.i0 < x.i1) {
+          // K's rows of keys that are left out become zeros: K is a factor of dS K
+          ok = guard.wait(bar.own_full, own & 1);
+          if (!ok) break;
+          ++own;
+          if (!tile_full(a, x.k0, x.count))
+            clear_rows<D>(sm + S::kOwn, key_bits(a, x.kb, x.k0, x.count, lane), min(128, a.Nk - x.k0), lane);
+          if (lane == 0) tc::mbar_arrive(bar.own_ready);
+        }
         for (long long j = x.i0; j < x.i1; ++j, ++n) {
           const RowTile r = row_tile(a, x, j, rtiles);
           const size_t head = ((size_t)r.b * a.Hq + r.h) * a.Nq;
@@ -365,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const KeyItem x = key_item(a, i, ktiles, rtiles);
         if (x.i0 >= x.i1) continue;
-        ok = guard.wait(bar.own_full, own_n & 1) && form(0) && form(1);
+        ok = guard.wait(kWithQ ? bar.own_ready : bar.own_full, own_n & 1) && form(0) && form(1);
         if (!ok) break;
         ++own_n;
         uint32_t more = 0;
@@ -392,6 +417,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           } else {
             tc::mma_commit(bar.a_empty + ta.slot);
             ta.step();
+            if constexpr (kWithQ) {  // dQ = dS K: the columns of dS^T as rows
+              const uint32_t buf = steps & 1;
+              ok = guard.wait(bar.dq_taken + buf, (steps >> 1 & 1) ^ 1);
+              if (!ok) break;
+              tc::tc_fence_after();
+              const uint64_t ds = tc::sdesc_sw128(tc::smem_u32(sm + S::kDS), 128 * 128, 1024);
+              const uint64_t own_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 128 * 128, 1024);
+              constexpr uint32_t idesc = tc::idesc_bf16(128, D, 1, 1);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc::mma_bf16(tQ + buf * D, ds + k * (2048 >> 4), own_mn + k * (2048 >> 4), idesc, k > 0);
+              tc::mma_commit(bar.dq_full + buf);
+            }
           }
           if (left == 1) tc::mma_commit(bar.done);
         }
@@ -409,8 +447,36 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
     const float2 c2 = fm::f2(c2f, c2f);
     uint32_t steps = 0, dones = 0;
     bool ok = true;
+    RowTile before{};  // the row tile of the step before, whose dQ is under way
+    // dQ of step n: its group (they take turns) writes the rows
+    auto write_q = [&](uint32_t n) {
+      const uint32_t buf = n & 1;
+      if (!guard.wait(bar.dq_full + buf, n >> 1 & 1)) return false;
+      tc::tc_fence_after();
+      if (half == (int)buf) {
+        store_block(tQ + buf * D + lane_off, a.scale, sm + S::kOutQ + warp * 4096, &maps.out2, 0,
+                    before.row0 + quarter * 32, a.Nq, a.Hq > 1 ? before.h : 0, a.B > 1 ? before.b : 0, lane);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar.dq_taken + buf);
+      }
+      return true;
+    };
     for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
       const KeyItem x = key_item(a, i, ktiles, rtiles);
+      if (kWithQ && x.count == 0) {  // no key: dQ = 0
+        const KeyItem y = key_item(a, i, ktiles, rtiles, true);
+        for (long long j = y.i0; j < y.i1; ++j) {
+          const RowTile r = row_tile(a, y, j, rtiles);
+          for (int e = threadIdx.x; e < 128 * D / 8; e += kWorkWarps * 32) {
+            const int row = r.row0 + e / (D / 8);
+            if (row < a.Nq)
+              *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dQ) +
+                                        (((size_t)r.b * a.Hq + r.h) * a.Nq + row) * D + e % (D / 8) * 8) =
+                  make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
       const int key = x.k0 + quarter * 32 + lane;
       const bool live = key_seen(a, x.kb, key, x.count);
       for (long long j = x.i0; j < x.i1; ++j, ++steps) {
@@ -448,6 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         tc::tmem_ld32(tP + lane_off + half * 64, r);
         tc::tmem_ld32(tP + lane_off + half * 64 + 32, r + 32);
         tc::tmem_wait_ld();
+        if (kWithQ && j > x.i0) {  // dQ of the step before has been formed from the last dS
+          ok = write_q(steps - 1);
+          if (!ok) break;
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t w[16];
@@ -464,6 +534,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
             w[e] = live ? pack_bf16x2(d.x, d.y) : 0u;
           }
           tc::tmem_st16(tP + lane_off + half * 64 + c * 16, w);
+          if constexpr (kWithQ) {
+            const int row = quarter * 32 + lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(sm + S::kDS + half * 16384 + row * 128 + (((c * 4 + e) ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
+        }
+        if constexpr (kWithQ) {
+          tc::fence_proxy_async_smem();
+          before = row_tile(a, x, j, rtiles);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -474,6 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         }
       }
       if (!ok) break;
+      if (kWithQ && x.i0 < x.i1) {
+        ok = write_q(steps - 1);
+        if (!ok) break;
+      }
       // group 0 writes dV, group 1 dK
       const bool any = x.i0 < x.i1;
       const uint32_t acc = (half == 0 ? tV : tK) + lane_off;
@@ -803,22 +888,22 @@ cudaError_t maps_of(const CrossArgs& a, Maps* m) {
   return e;
 }
 
-template <int D>
+template <int D, bool kWithQ>
 cudaError_t run_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   Maps m;
   const Strides s = dense(a.Bk, a.Hk, a.Nk, D);
   cudaError_t e = maps_of<D>(a, &m);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dV, s, a.Bk, a.Hk, a.Nk, D, 32);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, s, a.Bk, a.Hk, a.Nk, D, 32);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out2, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
   if (e != cudaSuccess) return e;
   constexpr int smem = Smem<D>::kTotal;
-  e = allow_smem<cross_tc_dkv_kernel<D>>(smem);
+  e = allow_smem<cross_tc_dkv_kernel<D, kWithQ>>(smem);
   if (e != cudaSuccess) return e;
   const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
-  const long long items = (long long)a.Bk * a.Hk * ktiles * a.splits;
-  const int grid = (int)(items < num_sms() ? items : num_sms());
-  cross_tc_dkv_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, (int)items, ktiles, rtiles);
-  return cudaGetLastError();
+  const int items = a.Bk * a.Hk * ktiles * a.splits;
+  const dim3 grid(items < num_sms() ? items : num_sms());
+  return launch_after(cross_tc_dkv_kernel<D, kWithQ>, grid, dim3(kThreads), smem, st, m, a, err, items, ktiles, rtiles);
 }
 
 template <int D>
@@ -827,7 +912,7 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, Launc
   cudaError_t e = maps_of<D>(a, &m);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
   if (e != cudaSuccess) return e;
-  m.out1 = m.out0;
+  m.out1 = m.out2 = m.out0;
   constexpr int smem = Smem<D>::kTotal;
   e = allow_smem<cross_tc_dq_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
@@ -843,9 +928,12 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, Launc
 
 }  // namespace
 
+bool cross_tc_dkv_forms_dq(int Nk, int d) { return d == 64 && Nk <= 128; }
+
 cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
-  log.add("cross_tc_dkv");
-  return a.d == 64 ? run_dkv<64>(a, err, st) : run_dkv<128>(a, err, st);
+  log.add(cross_tc_dkv_forms_dq(a.Nk, a.d) ? "cross_tc_dqkv" : "cross_tc_dkv");
+  if (cross_tc_dkv_forms_dq(a.Nk, a.d)) return run_dkv<64, true>(a, err, st);
+  return a.d == 64 ? run_dkv<64, false>(a, err, st) : run_dkv<128, false>(a, err, st);
 }
 cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   log.add("cross_tc_dq");

@@ -176,7 +176,7 @@ constexpr long long kFewRows = 32;
 // tiles, fill its rounds: the items of full rounds stay whole, those of the last
 // round are split where two or more parts of at least four tiles each fit it.
 // 64 pairs of row tiles of each of 8 heads of 128 over 16384 keys (3.46 rounds): 990
-// us whole, 895 us with the last round split in two.
+// us whole, 909 us with the last round split in two.
 struct Rounds {
   int whole = 0, splits = 1;
   long long parts = 0;  // partial results
@@ -467,17 +467,14 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   if (e == cudaSuccess && s.Nk > 0) {
     a.splits = p.dkv_splits;
     e = p.tc ? launch_cross_tc_dkv(a, err, cs, log) : launch_cross_simt_dkv(a, dtype, cs, log);
-    if (a.splits > 1) {
-      if (e == cudaSuccess) e = launch_partial_sum(dtype, a.part, 2 * kn, a.splits, dK, kn, cs, log);
-      if (e == cudaSuccess) e = launch_partial_sum(dtype, a.part + kn, 2 * kn, a.splits, dV, kn, cs, log);
-    }
+    void* const outs[2] = {dK, dV};
+    if (e == cudaSuccess && a.splits > 1) e = launch_partial_sum(dtype, a.part, a.splits, outs, 2, kn, cs, log);
   }
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && !(p.tc && cross_tc_dkv_forms_dq(s.Nk, s.d))) {
     a.splits = p.tc ? p.rounds.splits : p.dq_splits;
     a.whole = p.rounds.whole;
     e = p.tc ? launch_cross_tc_dq(a, err, cs, log) : launch_cross_simt_dq(a, dtype, cs, log);
-    if (e == cudaSuccess && p.dq_splits > 1)
-      e = launch_partial_sum(dtype, a.part, qn, p.dq_splits, dQ, qn, cs, log);
+    if (e == cudaSuccess && p.dq_splits > 1) e = launch_partial_sum(dtype, a.part, p.dq_splits, &dQ, 1, qn, cs, log);
   }
   return api_finish(e, "cross attention backward launch", log);
 }

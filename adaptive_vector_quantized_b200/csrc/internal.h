@@ -158,8 +158,9 @@ cudaError_t launch_cross_join(const CrossArgs& a, avq_dtype dt, cudaStream_t st,
 // all, `per_head` of them to a head.  softmax: O and lse, else dQ by sums.
 cudaError_t launch_cross_join_items(const CrossArgs& a, int items, int per_head, int rows, bool softmax,
                                     cudaStream_t st, LaunchLog& log);
-// out[i] = sum over s < splits of part[s * stride + i], i < n (a multiple of 4).
-cudaError_t launch_partial_sum(avq_dtype dt, const float* part, size_t stride, int splits, void* out, size_t n,
+// out[o][i] = sum over s < splits of part[(s * outs + o) * n + i], o < outs (1 or
+// 2), i < n (a multiple of 4).
+cudaError_t launch_partial_sum(avq_dtype dt, const float* part, int splits, void* const* out, int outs, size_t n,
                                cudaStream_t st, LaunchLog& log);
 // delta = rowsum(dO O)
 cudaError_t launch_cross_delta(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
@@ -181,6 +182,8 @@ cudaError_t make_tmap_view_bf16(CUtensorMap* map, const void* base, const Stride
 // Tensor-core kernels of the cross attention (bf16).
 cudaError_t launch_cross_few(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_tc(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
+// With one key tile and d = 64 the first of the two writes dQ as well.
+bool cross_tc_dkv_forms_dq(int Nk, int d);
 cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
 
