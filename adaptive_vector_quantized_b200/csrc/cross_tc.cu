@@ -376,14 +376,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         if (!ok) break;
         s_phase ^= 1u << half;
         tc::tc_fence_after();
+        const bool upper = whole || k0 + 32 < end;  // the last step may have keys in its first 32 columns alone
         uint32_t r[kStep];
         tc::tmem_ld32(sS, r);
-        tc::tmem_ld32(sS + 32, r + 32);
+        if (upper) tc::tmem_ld32(sS + 32, r + 32);
         tc::tmem_wait_ld();
         if (!whole) {
 #pragma unroll
-          for (int k = 0; k < kStep; ++k)
-            if (!(bits[k >> 5] >> (k & 31) & 1u)) r[k] = 0xff800000u;  // whatever stands there
+          for (int c = 0; c < 2; ++c)
+            if (bits[c] != 0xffffffffu) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(bits[c] >> k & 1u)) r[c * 32 + k] = 0xff800000u;  // whatever stands there
+            }
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -425,8 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[16];
-          if (whole) exp_chunk<false>(r + c * 32, c2, nbase, p, sum);
-          else exp_chunk<true>(r + c * 32, c2, nbase, p, sum);
+          if (whole) {
+            exp_chunk<false>(r + c * 32, c2, nbase, p, sum);
+          } else {
+            if (c == 1 && !upper) break;
+            exp_chunk<true>(r + c * 32, c2, nbase, p, sum);
+          }
           tc::tmem_st16(sS + c * 16, p);
         }
         tc::tmem_wait_st();
