@@ -39,6 +39,12 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Where part `split` of `parts` of n units begins (split == parts: where the last
+// ends).  A 64-bit division takes hundreds of clocks: not for what is whole.
+__device__ __forceinline__ int part_begin(int n, int split, int parts) {
+  return split == 0 ? 0 : split == parts ? n : (int)((long long)n * split / parts);
+}
+
 template <typename T>
 __device__ __forceinline__ void put4(T* p, const float* v);
 template <>

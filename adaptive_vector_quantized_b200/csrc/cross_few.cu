@@ -60,7 +60,7 @@ struct RowAt {
   int b, h, n;
 };
 __device__ __forceinline__ RowAt row_at(const CrossArgs& a, int kb, int kh, int r) {
-  const int R = a.B / a.Bk, G = a.Hq / a.Hk;
+  const int R = a.per_b, G = a.per_h;
   const int rg = r / a.Nq;
   return RowAt{kb * R + rg / G, kh * G + rg % G, r % a.Nq};
 }
@@ -78,8 +78,8 @@ __device__ __forceinline__ Item item_of(const CrossArgs& a, int i, int chunks) {
   x.kh = kvh % a.Hk;
   x.count = key_count(a, x.kb);
   const int tiles = (x.count + kTile - 1) / kTile;
-  x.t0 = (int)((long long)tiles * x.split / a.splits);
-  x.t1 = (int)((long long)tiles * (x.split + 1) / a.splits);
+  x.t0 = part_begin(tiles, x.split, a.splits);
+  x.t1 = part_begin(tiles, x.split + 1, a.splits);
   return x;
 }
 
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
     return;
   }
 
-  const int rows = (a.B / a.Bk) * (a.Hq / a.Hk) * a.Nq;
+  const int rows = a.per_b * a.per_h * a.Nq;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // 16-byte piece c of row r of a [64 keys][D] tile
   auto piece = [&](const uint8_t* tile, int r, int c) {
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
 
 template <int D, int ROWS>
 cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
-  const int rows = (a.B / a.Bk) * (a.Hq / a.Hk) * a.Nq;
+  const int rows = a.per_b * a.per_h * a.Nq;
   const int chunks = (rows + ROWS - 1) / ROWS;
   CUtensorMap k, v;
   cudaError_t e = make_tmap_view_bf16(&k, a.K, a.ks, a.Bk, a.Hk, a.Nk, D, kTile);
@@ -337,7 +337,7 @@ cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
 
 cudaError_t launch_cross_few(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   log.add("cross_few");
-  const int rows = (a.B / a.Bk) * (a.Hq / a.Hk) * a.Nq;
+  const int rows = a.per_b * a.per_h * a.Nq;
   if (rows <= 8) return a.d == 64 ? run<64, 8>(a, err, st) : run<128, 8>(a, err, st);
   return a.d == 64 ? run<64, 16>(a, err, st) : run<128, 16>(a, err, st);
 }

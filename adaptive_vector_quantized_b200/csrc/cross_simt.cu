@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(kThreads) cross_simt_kernel(const CrossArgs a)
   const int tiles = (a.Nq + kT - 1) / kT;
   const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
   const int b = bh / a.Hq, h = bh % a.Hq;
-  const int kb = b / (a.B / a.Bk), kh = h / (a.Hq / a.Hk);
+  const int kb = b / a.per_b, kh = h / a.per_h;
   const int count = key_count(a, kb);
   const int ktiles = (count + kT - 1) / kT;
-  const int t0 = (int)((long long)ktiles * split / a.splits), t1 = (int)((long long)ktiles * (split + 1) / a.splits);
+  const int t0 = part_begin(ktiles, split, a.splits), t1 = part_begin(ktiles, split + 1, a.splits);
   const int row0 = rt * kT;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const T* Q = static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArg
   const int tiles = (a.Nk + kT - 1) / kT;
   const int kt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
   const int kb = bh / a.Hk, kh = bh % a.Hk;
-  const int R = a.B / a.Bk, G = a.Hq / a.Hk;
+  const int R = a.per_b, G = a.per_h;
   const int k0 = kt * kT;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const int count = key_count(a, kb);
@@ -270,10 +270,10 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArg
   clear<D>(dk);
   clear<D>(dv);
   const int rtiles = (a.Nq + kT - 1) / kT;
-  const long long all = (long long)R * G * rtiles;
-  const long long i0 = all * split / a.splits, i1 = k0 < count ? all * (split + 1) / a.splits : i0;
-  for (long long it = i0; it < i1; ++it) {
-    const int row0 = (int)(it % rtiles) * kT, rg = (int)(it / rtiles);
+  const int all = R * G * rtiles;
+  const int i0 = part_begin(all, split, a.splits), i1 = k0 < count ? part_begin(all, split + 1, a.splits) : i0;
+  for (int it = i0; it < i1; ++it) {
+    const int row0 = it % rtiles * kT, rg = it / rtiles;
     const int b = kb * R + rg / G, h = kh * G + rg % G;
     __syncthreads();
     load_tile<T, D>(sQ, static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h, a.qs.n, row0,
@@ -329,12 +329,12 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dq_kernel(const CrossArgs
   const int tiles = (a.Nq + kT - 1) / kT;
   const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
   const int b = bh / a.Hq, h = bh % a.Hq;
-  const int kb = b / (a.B / a.Bk), kh = h / (a.Hq / a.Hk);
+  const int kb = b / a.per_b, kh = h / a.per_h;
   const int row0 = rt * kT;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const int count = key_count(a, kb);
   const int ktiles = (count + kT - 1) / kT;
-  const int t0 = (int)((long long)ktiles * split / a.splits), t1 = (int)((long long)ktiles * (split + 1) / a.splits);
+  const int t0 = part_begin(ktiles, split, a.splits), t1 = part_begin(ktiles, split + 1, a.splits);
   load_tile<T, D>(sQ, static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h, a.qs.n, row0,
                   [&](int r) { return row0 + r < a.Nq; });
   load_tile<T, D>(sG, static_cast<const T*>(a.G) + b * a.gs.b + h * a.gs.h, a.gs.n, row0,

@@ -73,17 +73,17 @@ __device__ __forceinline__ Item item_of(const CrossArgs& a, int i, int pairs) {
   Item x;
   const Part part = part_of(a, i);
   x.parts = part.parts;
-  const int pair = part.item % pairs, bh = part.item / pairs;
+  const int bh = part.item / pairs, pair = part.item - bh * pairs;
   x.b = bh / a.Hq;
-  x.h = bh % a.Hq;
-  x.kb = x.b / (a.B / a.Bk);
-  x.kh = x.h / (a.Hq / a.Hk);
+  x.h = bh - x.b * a.Hq;
+  x.kb = x.b / a.per_b;
+  x.kh = x.h / a.per_h;
   x.row0 = pair * 2 * kRowTile;
   x.tiles = x.row0 + kRowTile < a.Nq ? 2 : 1;
   x.count = key_count(a, x.kb);
   const int kt = (x.count + kKeyTile - 1) / kKeyTile;
-  x.t0 = (int)((long long)kt * part.split / part.parts);
-  x.t1 = (int)((long long)kt * (part.split + 1) / part.parts);
+  x.t0 = part_begin(kt, part.split, part.parts);
+  x.t1 = part_begin(kt, part.split + 1, part.parts);
   return x;
 }
 

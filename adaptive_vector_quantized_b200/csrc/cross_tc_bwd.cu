@@ -220,7 +220,7 @@ __device__ __forceinline__ void store_partial(uint32_t taddr, float f, float* ds
 
 struct KeyItem {
   int kb, kh, k0, count, split;
-  long long i0, i1;  // row tiles of the query heads and entries that share the key head
+  int i0, i1;  // row tiles of the query heads and entries that share the key head
 };
 // any_rows: also of a tile with no key (its rows' dQ are written here).
 __device__ __forceinline__ KeyItem key_item(const CrossArgs& a, int i, int ktiles, int rtiles, bool any_rows = false) {
@@ -232,18 +232,17 @@ __device__ __forceinline__ KeyItem key_item(const CrossArgs& a, int i, int ktile
   x.kb = bh / a.Hk;
   x.kh = bh % a.Hk;
   x.count = key_count(a, x.kb);
-  const long long all = any_rows || x.k0 < x.count ? (long long)(a.B / a.Bk) * (a.Hq / a.Hk) * rtiles : 0;
-  x.i0 = all * x.split / a.splits;
-  x.i1 = all * (x.split + 1) / a.splits;
+  const int all = any_rows || x.k0 < x.count ? a.per_b * a.per_h * rtiles : 0;
+  x.i0 = part_begin(all, x.split, a.splits);
+  x.i1 = part_begin(all, x.split + 1, a.splits);
   return x;
 }
 struct RowTile {
   int b, h, row0;
 };
-__device__ __forceinline__ RowTile row_tile(const CrossArgs& a, const KeyItem& x, long long i, int rtiles) {
-  const int R = a.B / a.Bk, G = a.Hq / a.Hk;
-  const int rg = (int)(i / rtiles);
-  return RowTile{x.kb * R + rg / G, x.kh * G + rg % G, (int)(i % rtiles) * 128};
+__device__ __forceinline__ RowTile row_tile(const CrossArgs& a, const KeyItem& x, int i, int rtiles) {
+  const int rg = i / rtiles;
+  return RowTile{x.kb * a.per_b + rg / a.per_h, x.kh * a.per_h + rg % a.per_h, (i - rg * rtiles) * 128};
 }
 
 template <int D, bool kWithQ>
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           load_tile<D>(sm + S::kOwn, &maps.k, a.ks, x.k0, x.kh, x.kb, bar.own_full);
           load_tile<D>(sm + S::kOwn + S::kTileBytes, &maps.v, a.vs, x.k0, x.kh, x.kb, bar.own_full);
           ++own;
-          for (long long j = x.i0; j < x.i1; ++j) {
+          for (int j = x.i0; j < x.i1; ++j) {
             const RowTile r = row_tile(a, x, j, rtiles);
             ok = guard.wait(bar.a_empty + ta.slot, ta.phase ^ 1);
             if (!ok) break;
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
             clear_rows<D>(sm + S::kOwn, key_bits(a, x.kb, x.k0, x.count, lane), min(128, a.Nk - x.k0), lane);
           if (lane == 0) tc::mbar_arrive(bar.own_ready);
         }
-        for (long long j = x.i0; j < x.i1; ++j, ++n) {
+        for (int j = x.i0; j < x.i1; ++j, ++n) {
           const RowTile r = row_tile(a, x, j, rtiles);
           const size_t head = ((size_t)r.b * a.Hq + r.h) * a.Nq;
           float l[4], d[4];
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         if (!ok) break;
         ++own_n;
         uint32_t more = 0;
-        for (int left = (int)(x.i1 - x.i0); left > 0 && ok; --left, ++steps) {
+        for (int left = x.i1 - x.i0; left > 0 && ok; --left, ++steps) {
           ok = second ? guard.wait(bar.a_full + ta.slot, ta.phase) : guard.wait(bar.b_full + tb.slot, tb.phase);
           if (!ok) break;
 #pragma unroll
@@ -466,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       const KeyItem x = key_item(a, i, ktiles, rtiles);
       if (kWithQ && x.count == 0) {  // no key: dQ = 0
         const KeyItem y = key_item(a, i, ktiles, rtiles, true);
-        for (long long j = y.i0; j < y.i1; ++j) {
+        for (int j = y.i0; j < y.i1; ++j) {
           const RowTile r = row_tile(a, y, j, rtiles);
           for (int e = threadIdx.x; e < 128 * D / 8; e += kWorkWarps * 32) {
             const int row = r.row0 + e / (D / 8);
@@ -479,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       }
       const int key = x.k0 + quarter * 32 + lane;
       const bool live = key_seen(a, x.kb, key, x.count);
-      for (long long j = x.i0; j < x.i1; ++j, ++steps) {
+      for (int j = x.i0; j < x.i1; ++j, ++steps) {
         const float* rows = sRows + (steps & 1) * 256 + half * 64;
         ok = guard.wait(bar.rows_full + (steps & 1), steps >> 1 & 1) && guard.wait(bar.s_full + half, steps & 1);
         if (!ok) break;
@@ -617,12 +616,12 @@ __device__ __forceinline__ RowItem row_item(const CrossArgs& a, int i, int rtile
   const int bh = part.item / rtiles;
   x.b = bh / a.Hq;
   x.h = bh % a.Hq;
-  x.kb = x.b / (a.B / a.Bk);
-  x.kh = x.h / (a.Hq / a.Hk);
+  x.kb = x.b / a.per_b;
+  x.kh = x.h / a.per_h;
   x.count = key_count(a, x.kb);
   const int kt = (x.count + 127) / 128;
-  x.t0 = (int)((long long)kt * part.split / part.parts);
-  x.t1 = (int)((long long)kt * (part.split + 1) / part.parts);
+  x.t0 = part_begin(kt, part.split, part.parts);
+  x.t1 = part_begin(kt, part.split + 1, part.parts);
   return x;
 }
 

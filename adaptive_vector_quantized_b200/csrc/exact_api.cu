@@ -266,6 +266,7 @@ avq_status cross_inputs(const avq_cross_dims& s, avq_dtype dt, const void* Q, co
   }
   if (!aligned(kv_lens, 4)) return api_fail(AVQ_ERR_INVALID_ARG, "kv_lens is not 4-byte aligned");
   a->B = s.B, a->Bk = s.Bk, a->Hq = s.Hq, a->Hk = s.Hk, a->Nq = s.Nq, a->Nk = s.Nk, a->d = s.d;
+  a->per_b = s.B / s.Bk, a->per_h = s.Hq / s.Hk;
   a->scale = s.scale;
   a->splits = 1;
   a->Q = Q, a->K = K, a->V = V;

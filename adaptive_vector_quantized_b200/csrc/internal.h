@@ -139,6 +139,7 @@ cudaError_t launch_qk_norm_backward(const avq_qk_dims& s, avq_dtype dt, const vo
 // tiles, or pairs of them) that are not split.
 struct CrossArgs {
   int B, Bk, Hq, Hk, Nq, Nk, d;
+  int per_b, per_h;  // batch entries to an encoder sequence, query heads to a key head
   float scale;
   int splits, whole;
   Strides qs, ks, vs, os, gs;
