@@ -10,8 +10,8 @@
 // A block has two groups of four warps for the elementwise work (a TMEM lane to
 // a thread, half of the tile's columns to a group), a warp that loads by TMA, one
 // that fetches lse and delta (dK/dV) or clears K's rows of keys that are left
-// out (dQ), and two threads that issue the MMAs of a chain each, since what a
-// thread does between MMAs would leave the tensor pipe idle.  P and dS overwrite
+// out (dQ), and two that issue the MMAs of a chain each, since what a warp does
+// between MMAs would leave the tensor pipe idle.  P and dS overwrite
 // S and dP in TMEM as bf16 and are first operands from there.
 //   dK/dV:  S(j) -> P(j) -> dV(j), S(j+1)     dP(j) -> dS(j) -> dK(j), dP(j+1)
 //   dQ:     S(j), S(j+1) in turn              dP(j) -> dS(j) -> dQ(j), dP(j+1)
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
   float* sRows = reinterpret_cast<float*>(sm + S::kRows);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     init_bars<D>(bar, 2, kWorkWarps / 2, 2);
     *sAbort = 0;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           if (lane == 0) tc::mbar_arrive(bar.rows_full + (n & 1));
         }
       }
-    } else if (lane == 0) {
+    } else {
       const bool second = warp > kMmaWarp;  // the chain of dP
       const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
       const uint64_t ring_a = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingA), 16, 1024);
@@ -371,70 +371,82 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       auto form = [&](int half) {
         const uint32_t d = (second ? tP : tS) + half * 64;
         if (!second) {
-          if (half == 0 && !guard.wait(bar.a_full + ta1.slot, ta1.phase)) return false;
-          mma_rows_rows<D, 64>(d, own, ring_a + ta1.slot * kTile16 + half * kHalf16);
-          tc::mma_commit(bar.s_full + half);
+          if (half == 0 && !wait_all(guard, bar.a_full + ta1.slot, ta1.phase)) return false;
+          if (tc::elect_one()) {
+            mma_rows_rows<D, 64>(d, own, ring_a + ta1.slot * kTile16 + half * kHalf16);
+            tc::mma_commit(bar.s_full + half);
+          }
           if (half == 1) ta1.step();
         } else {
-          if (half == 0 && !guard.wait(bar.b_full + tb1.slot, tb1.phase)) return false;
-          mma_rows_rows<D, 64>(d, own + kTile16, ring_b + tb1.slot * kTile16 + half * kHalf16);
-          tc::mma_commit(bar.dp_full + half);
-          if (half == 1) {
-            tc::mma_commit(bar.b_empty + tb1.slot);  // dO: the chain of S releases it too
-            tb1.step();
+          if (half == 0 && !wait_all(guard, bar.b_full + tb1.slot, tb1.phase)) return false;
+          if (tc::elect_one()) {
+            mma_rows_rows<D, 64>(d, own + kTile16, ring_b + tb1.slot * kTile16 + half * kHalf16);
+            tc::mma_commit(bar.dp_full + half);
+            if (half == 1) tc::mma_commit(bar.b_empty + tb1.slot);  // dO: the chain of S releases it too
           }
+          if (half == 1) tb1.step();
         }
         return true;
       };
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const KeyItem x = key_item(a, i, ktiles, rtiles);
-        if (x.i0 >= x.i1) continue;
-        ok = guard.wait(kWithQ ? bar.own_ready : bar.own_full, own_n & 1) && form(0) && form(1);
+        const int tiles = uniform(x.i1 - x.i0);
+        if (tiles <= 0) continue;
+        ok = wait_all(guard, kWithQ ? bar.own_ready : bar.own_full, own_n & 1) && form(0) && form(1);
         if (!ok) break;
         ++own_n;
         uint32_t more = 0;
-        for (int left = x.i1 - x.i0; left > 0 && ok; --left, ++steps) {
-          ok = second ? guard.wait(bar.a_full + ta.slot, ta.phase) : guard.wait(bar.b_full + tb.slot, tb.phase);
+        for (int left = tiles; left > 0 && ok; --left, ++steps) {
+          uint64_t* const full = second ? bar.a_full + ta.slot : bar.b_full + tb.slot;
+          ok = wait_all(guard, full, second ? ta.phase : tb.phase);
           if (!ok) break;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            ok = guard.wait((second ? bar.ds_ready : bar.p_ready) + half, steps & 1);
+            ok = wait_all(guard, (second ? bar.ds_ready : bar.p_ready) + half, steps & 1);
             if (!ok) break;
             tc::tc_fence_after();
-            if (!second)  // dV += P^T dO
-              mma_tmem_cols<D>(tV, tS + half * 64, ring_b_mn + tb.slot * kTile16 + half * kHalf16, more);
-            else  // dK += dS^T Q
-              mma_tmem_cols<D>(tK, tP + half * 64, ring_a_mn + ta.slot * kTile16 + half * kHalf16, more);
+            if (tc::elect_one()) {
+              if (!second) {  // dV += P^T dO
+                mma_tmem_cols<D>(tV, tS + half * 64, ring_b_mn + tb.slot * kTile16 + half * kHalf16, more);
+              } else {  // dK += dS^T Q
+                mma_tmem_cols<D>(tK, tP + half * 64, ring_a_mn + ta.slot * kTile16 + half * kHalf16, more);
+              }
+            }
             more = 1;
             if (left > 1) ok = form(half);
             if (!ok) break;
           }
           if (!ok) break;
           if (!second) {
-            tc::mma_commit(bar.b_empty + tb.slot);
+            if (tc::elect_one()) tc::mma_commit(bar.b_empty + tb.slot);
             tb.step();
           } else {
-            tc::mma_commit(bar.a_empty + ta.slot);
+            if (tc::elect_one()) tc::mma_commit(bar.a_empty + ta.slot);
             ta.step();
             if constexpr (kWithQ) {  // dQ = dS K: the columns of dS^T as rows
               const uint32_t buf = steps & 1;
-              ok = guard.wait(bar.dq_taken + buf, (steps >> 1 & 1) ^ 1);
+              ok = wait_all(guard, bar.dq_taken + buf, (steps >> 1 & 1) ^ 1);
               if (!ok) break;
               tc::tc_fence_after();
               const uint64_t ds = tc::sdesc_sw128(tc::smem_u32(sm + S::kDS), 128 * 128, 1024);
               const uint64_t own_mn = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 128 * 128, 1024);
               constexpr uint32_t idesc = tc::idesc_bf16(128, D, 1, 1);
+              if (tc::elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tc::mma_bf16(tQ + buf * D, ds + k * (2048 >> 4), own_mn + k * (2048 >> 4), idesc, k > 0);
-              tc::mma_commit(bar.dq_full + buf);
+                for (int k = 0; k < 8; ++k)
+                  tc::mma_bf16(tQ + buf * D, ds + k * (2048 >> 4), own_mn + k * (2048 >> 4), idesc, k > 0);
+                tc::mma_commit(bar.dq_full + buf);
+              }
             }
           }
-          if (left == 1) tc::mma_commit(bar.done);
+          if (left == 1) {
+            if (tc::elect_one()) tc::mma_commit(bar.done);
+          }
         }
       }
       uint64_t* drain = bar.drain + second;
-      tc::mma_commit(drain);
+      if (tc::elect_one()) tc::mma_commit(drain);
+      __syncwarp();
       tc::mbar_wait(drain, 0, 1000000ull);
     }
   } else {
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
   const Bars bar = bars_of<D>(sm);
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     init_bars<D>(bar, 1, kWorkWarps, 1);
     *sAbort = 0;
@@ -707,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
           if (lane == 0) tc::mbar_arrive(bar.a_ready + ta.slot);
         }
       }
-    } else if (lane == 0) {
+    } else {
       const bool second = warp > kMmaWarp;  // the chain of dP
       const uint64_t own = tc::sdesc_sw128(tc::smem_u32(sm + S::kOwn), 16, 1024);
       const uint64_t ring_a = tc::sdesc_sw128(tc::smem_u32(sm + S::kRingA), 16, 1024);
@@ -719,52 +731,58 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
       uint32_t own_n = 0, steps = 0;
       bool ok = true;
       auto gradient = [&] {  // dP = dO V^T
-        if (!guard.wait(bar.b_full + tb.slot, tb.phase)) return false;
-        mma_rows_rows<D, 128>(tP, own + kTile16, ring_b + tb.slot * kTile16);
-        tc::mma_commit(bar.dp_full);
-        tc::mma_commit(bar.b_empty + tb.slot);
+        if (!wait_all(guard, bar.b_full + tb.slot, tb.phase)) return false;
+        if (tc::elect_one()) {
+          mma_rows_rows<D, 128>(tP, own + kTile16, ring_b + tb.slot * kTile16);
+          tc::mma_commit(bar.dp_full);
+          tc::mma_commit(bar.b_empty + tb.slot);
+        }
         tb.step();
         return true;
       };
       for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const RowItem x = row_item(a, i, rtiles);
-        if (x.t0 >= x.t1) continue;
-        ok = guard.wait(bar.own_full, own_n & 1);
+        const int tiles = uniform(x.t1 - x.t0);
+        if (tiles <= 0) continue;
+        ok = wait_all(guard, bar.own_full, own_n & 1);
         if (!ok) break;
         ++own_n;
         if (second) {
           ok = gradient();
           uint32_t more = 0;
-          for (int left = x.t1 - x.t0; left > 0 && ok; --left, ++steps) {
-            ok = guard.wait(bar.a_ready + ta.slot, ta.phase) && guard.wait(bar.ds_ready, steps & 1) &&
-                 guard.wait(bar.ds_ready + 1, steps & 1);
+          for (int left = tiles; left > 0 && ok; --left, ++steps) {
+            ok = wait_all(guard, bar.a_ready + ta.slot, ta.phase) && wait_all(guard, bar.ds_ready, steps & 1) &&
+                 wait_all(guard, bar.ds_ready + 1, steps & 1);
             if (!ok) break;
             tc::tc_fence_after();
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // dQ += dS K
-              mma_tmem_cols<D>(tQ, tP + half * 64, ring_a_mn + ta.slot * kTile16 + half * kHalf16, more);
-              more = 1;
+            if (tc::elect_one()) {  // dQ += dS K
+              mma_tmem_cols<D>(tQ, tP, ring_a_mn + ta.slot * kTile16, more);
+              mma_tmem_cols<D>(tQ, tP + 64, ring_a_mn + ta.slot * kTile16 + kHalf16, 1);
+              tc::mma_commit(bar.a_empty + ta.slot);
+              if (left == 1) tc::mma_commit(bar.done);
             }
-            tc::mma_commit(bar.a_empty + ta.slot);
+            more = 1;
             ta.step();
             if (left > 1) ok = gradient();
-            else tc::mma_commit(bar.done);
           }
         } else {
           // S of each step in the half of TMEM that the step before the last has left
-          for (int left = x.t1 - x.t0; left > 0; --left, ++steps) {
-            ok = guard.wait(bar.a_ready + ta.slot, ta.phase) &&
-                 guard.wait(bar.p_ready + (steps & 1), (steps >> 1 & 1) ^ 1);
+          for (int left = tiles; left > 0; --left, ++steps) {
+            ok = wait_all(guard, bar.a_ready + ta.slot, ta.phase) &&
+                 wait_all(guard, bar.p_ready + (steps & 1), (steps >> 1 & 1) ^ 1);
             if (!ok) break;
             tc::tc_fence_after();
-            mma_rows_rows<D, 128>(tmem + (steps & 1) * 128, own, ring_a + ta.slot * kTile16);
-            tc::mma_commit(bar.s_full + (steps & 1));
+            if (tc::elect_one()) {
+              mma_rows_rows<D, 128>(tmem + (steps & 1) * 128, own, ring_a + ta.slot * kTile16);
+              tc::mma_commit(bar.s_full + (steps & 1));
+            }
             ta.step();
           }
         }
       }
       uint64_t* drain = bar.drain + second;
-      tc::mma_commit(drain);
+      if (tc::elect_one()) tc::mma_commit(drain);
+      __syncwarp();
       tc::mbar_wait(drain, 0, 1000000ull);
     }
   } else {
