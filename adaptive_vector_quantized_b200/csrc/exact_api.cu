@@ -169,8 +169,11 @@ int split_count(long long items, long long units, long long target) {
 }
 long long tiles64(long long n) { return (n + 63) / 64; }
 
-// Rows per key head up to which the keys are streamed through registers.
-constexpr long long kFewRows = 32;
+// Rows per key head up to which mma.sync on 16 rows at a time beats the 128-row
+// tiles of tcgen05: with 32 sequences of 4096 keys, 8 key heads, 16 rows take 53
+// against 93 us at d = 64 and 91 against 99 at d = 128, 32 rows 78 against 93 and
+// 125 against 99.
+constexpr long long few_rows(int d) { return d == 64 ? 32 : 16; }
 
 // How the items of a kernel with one block per SM, each a walk over `units` key
 // tiles, fill its rounds: the items of full rounds stay whole, those of the last
@@ -217,7 +220,7 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   const long long key_tiles = (s.Nk + 127) / 128;
   p.tc = dt == AVQ_BF16 && api_path() != AVQ_PATH_SIMT && s.Nk > 0;
   if (!backward) {
-    p.few = p.tc && shared * s.Nq <= kFewRows;
+    p.few = p.tc && shared * s.Nq <= few_rows(s.d);
     if (p.tc && !p.few) {  // pairs of 128-row tiles
       p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 255) / 256), key_tiles);
       p.part = up256((size_t)p.rounds.parts * 256 * s.d * 4);
