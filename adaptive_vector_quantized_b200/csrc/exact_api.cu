@@ -23,9 +23,13 @@ avq_status need_ptr(const void* p, const char* name) {
   return AVQ_OK;
 }
 
+// What a view is for: its tokens may repeat (stride 0), it is read by tensor
+// copies (which cannot repeat rows), or it is written.
+enum Use { kRead, kCopied, kWritten };
+
 // Strides of a [B,H,N,d] view, those of dimensions of size 1 set to 0; the
 // tensor's extent in bytes in *span.
-avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, bool output, const char* name,
+avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, Use use, const char* name,
                 Strides* out, size_t* span) {
   if (s == nullptr) return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides are NULL", name);
   const int64_t v[3] = {B > 1 ? s->b : 0, H > 1 ? s->h : 0, N > 1 ? s->n : 0};
@@ -37,7 +41,9 @@ avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, 
       return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be in [0, 2^38)", name);
     if (v[i] * es % 16 != 0)
       return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", name);
-    if (output && n[i] > 1 && v[i] < d)
+    if (use == kCopied && i == 2 && N > 1 && v[i] == 0)
+      return api_fail(AVQ_ERR_INVALID_ARG, "%s: tokens must not repeat (stride 0)", name);
+    if (use == kWritten && n[i] > 1 && v[i] < d)
       return api_fail(AVQ_ERR_INVALID_ARG, "%s: an output's heads must not overlap", name);
     last += v[i] * (int64_t)(n[i] > 0 ? n[i] - 1 : 0);
   }
@@ -110,11 +116,11 @@ avq_status pair_of(const avq_qk_dims& s, avq_dtype dt, const void* q, const avq_
                    const void* k, const avq_strides* ks, const char* kn, Pair* out) {
   *out = Pair{};
   AVQ_TRY(need_ptr(q, qn));
-  AVQ_TRY(view(qs, s.B, s.Hq, s.N, s.d, dt, false, qn, &out->s[0], &out->span[0]));
+  AVQ_TRY(view(qs, s.B, s.Hq, s.N, s.d, dt, kRead, qn, &out->s[0], &out->span[0]));
   out->x[0] = q;
   if (s.Hk > 0) {
     AVQ_TRY(need_ptr(k, kn));
-    AVQ_TRY(view(ks, s.B, s.Hk, s.N, s.d, dt, false, kn, &out->s[1], &out->span[1]));
+    AVQ_TRY(view(ks, s.B, s.Hk, s.N, s.d, dt, kRead, kn, &out->s[1], &out->span[1]));
     out->x[1] = k;
   }
   return AVQ_OK;
@@ -258,12 +264,12 @@ avq_status cross_inputs(const avq_cross_dims& s, avq_dtype dt, const void* Q, co
                         const avq_strides* ks, const void* V, const avq_strides* vs, const int32_t* kv_lens,
                         const uint8_t* key_mask, CrossArgs* a, size_t* spans) {
   AVQ_TRY(need_ptr(Q, "Q"));
-  AVQ_TRY(view(qs, s.B, s.Hq, s.Nq, s.d, dt, false, "Q", &a->qs, &spans[0]));
+  AVQ_TRY(view(qs, s.B, s.Hq, s.Nq, s.d, dt, kCopied, "Q", &a->qs, &spans[0]));
   if (s.Nk > 0) {
     AVQ_TRY(need_ptr(K, "K"));
     AVQ_TRY(need_ptr(V, "V"));
-    AVQ_TRY(view(ks, s.Bk, s.Hk, s.Nk, s.d, dt, false, "K", &a->ks, &spans[1]));
-    AVQ_TRY(view(vs, s.Bk, s.Hk, s.Nk, s.d, dt, false, "V", &a->vs, &spans[2]));
+    AVQ_TRY(view(ks, s.Bk, s.Hk, s.Nk, s.d, dt, kCopied, "K", &a->ks, &spans[1]));
+    AVQ_TRY(view(vs, s.Bk, s.Hk, s.Nk, s.d, dt, kCopied, "V", &a->vs, &spans[2]));
   } else {
     spans[1] = spans[2] = 0;
   }
@@ -386,7 +392,7 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   size_t spans[3], ospan;
   AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
   AVQ_TRY(need_ptr(O, "O"));
-  AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, true, "O", &a.os, &ospan));
+  AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, kWritten, "O", &a.os, &ospan));
   const void* ins[3] = {Q, K, V};
   for (int i = 0; i < 3; ++i)
     if (spans[i] > 0 && overlap(O, ospan, ins[i], spans[i])) return api_fail(AVQ_ERR_INVALID_ARG, "O overlaps an input");
@@ -431,9 +437,9 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   size_t spans[5];
   AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
   AVQ_TRY(need_ptr(dO, "dO"));
-  AVQ_TRY(view(do_strides, s.B, s.Hq, s.Nq, s.d, dtype, false, "dO", &a.gs, &spans[3]));
+  AVQ_TRY(view(do_strides, s.B, s.Hq, s.Nq, s.d, dtype, kCopied, "dO", &a.gs, &spans[3]));
   AVQ_TRY(need_ptr(O, "O"));
-  AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, false, "O", &a.os, &spans[4]));
+  AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, kCopied, "O", &a.os, &spans[4]));
   AVQ_TRY(need_ptr(lse, "lse"));
   AVQ_TRY(need_ptr(dQ, "dQ"));
   if (s.Nk > 0) {

@@ -341,8 +341,9 @@ avq_status avq_gilbert_order(int width, int height, int32_t* idx);
 
 /* Strides, in elements, of batch entry, head and token of a [B,H,N,d] tensor
  * whose last dimension is contiguous.  Each times the element size must be a
- * multiple of 16 bytes, and none negative (0 repeats the same data; not for
- * outputs).  The stride of a dimension of size 1 is not used. */
+ * multiple of 16 bytes, and none negative.  0 repeats the same data: not for
+ * outputs, nor for the tokens of the cross attention's tensors.  The stride of
+ * a dimension of size 1 is not used. */
 typedef struct {
   int64_t b, h, n;
 } avq_strides;

@@ -104,6 +104,7 @@ def cross(dims=None, dt=avq.AVQ_BF16, Q=FAKE[0], qs=CQ, K=FAKE[1], ks=CK, V=FAKE
     (dict(dims=cd(scale=math.nan)), BAD), (dict(dt=2), BAD), (dict(Q=None), BAD), (dict(K=None), BAD),
     (dict(V=FAKE[2] + 2), BAD), (dict(O=None), BAD), (dict(O=FAKE[1] + 64), BAD), (dict(lens=FAKE[4] + 2), BAD),
     (dict(lse=FAKE[4] + 4), BAD), (dict(qs=avq.avq_strides(2560, 640, 65)), BAD),
+    (dict(qs=avq.avq_strides(2560, 640, 0)), BAD), (dict(ks=avq.avq_strides(2560, 1280, 0)), BAD),
     (dict(os_=avq.avq_strides(2560, 0, 64)), BAD), (dict(os_=avq.avq_strides(2560, 640, 32)), BAD),
 ])
 def test_cross_attention_refuses(kw, status):

@@ -234,9 +234,159 @@ def test_cross_refuses():
         avq.avq_cross_attention_backward(dO, Q, K, V, Q, None)
     with pytest.raises(ValueError):
         avq.avq_cross_attention(Q, K.transpose(2, 3), V)
+    with pytest.raises(avq.AVQError):  # repeated tokens
+        avq.avq_cross_attention(Q, K[:, :, :1].expand(2, 2, 20, 64), V)
+    O, lse = avq.avq_cross_attention(Q, K, V, lse=True)
+    with pytest.raises(avq.AVQError):
+        avq.avq_cross_attention_backward(dO[:, :, :1].expand(2, 4, 10, 64), Q, K, V, O, lse)
     old = avq.avq_set_path(avq.AVQ_PATH_TC)
     try:
         with pytest.raises(avq.AVQError):  # no tensor-core kernel for fp32
             avq.avq_cross_attention(Q, K, V)
     finally:
         avq.avq_set_path(old)
+
+
+def test_cross_repeated_inputs_backward():
+    """Repeated K and V (stride 0) have a gradient for every place; their sum is the shared form's."""
+    Q, K, V, dO, _ = inputs(4, 1, 6, 1, 90, 110, 64, torch.bfloat16, 9)
+    want = ref.cross(Q, K, V, dO=dO)
+    O, lse = want["O"].to(torch.bfloat16).cuda(), want["lse"].float().cuda()
+    Ke, Ve = K.expand(4, 6, 110, 64), V.expand(4, 6, 110, 64)
+    each = ref.cross(Q, Ke, Ve, dO=dO, O_given=O)
+    dQ, dK, dV = avq.avq_cross_attention_backward(dO, Q, Ke, Ve, O, lse)
+    for n, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
+        ref.check(n, t, each[n], each[n + "_tol"])
+    # a gradient that repeats over batch and heads
+    ones = dO[:1, :1].expand(4, 6, 90, 64)
+    flat = ref.cross(Q, K, V, dO=ones, O_given=O)
+    got = avq.avq_cross_attention_backward(ones, Q, K, V, O, lse)
+    for n, t in zip(("dQ", "dK", "dV"), got):
+        ref.check(n, t, flat[n], flat[n + "_tol"])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("Nq, Nk", [(1, 700), (150, 300)])
+def test_cross_nan_reaches_its_rows_alone(dtype, Nq, Nk):
+    """NaN in one query gives NaN in its row, infinity in a value that is looked at is not hidden, nothing else changes."""
+    Q, K, V, _, _ = inputs(2, 2, 3, 3, Nq, Nk, 64, DT[dtype], 11)
+    want = avq.avq_cross_attention(Q, K, V)[0]
+    Q[1, 2, Nq - 1, 5] = float("nan")
+    V[0, 1, Nk // 2, 7] = float("inf")
+    got = avq.avq_cross_attention(Q, K, V)[0]
+    assert torch.isnan(got[1, 2, Nq - 1]).all()
+    assert torch.isinf(got[0, 1, :, 7]).all()
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[1, 2, Nq - 1] = True
+    hit[0, 1, :, 7] = True
+    assert torch.equal(got[~hit], want[~hit])
+
+
+def rand_cases(n, seed):
+    """Shapes across the kernels' rules: rows from one to several tiles, keys from none to many tiles."""
+    import random
+
+    r = random.Random(seed)
+    out = []
+    for _ in range(n):
+        Hk, Bk = r.choice([1, 2, 3]), r.choice([1, 2, 3])
+        Nk = r.choice([1, 2, 63, 64, 65, 77, 127, 128, 129, r.randint(1, 128), r.randint(129, 1500)])
+        Nq = r.choice([1, 2, 7, 17, 33, 127, 128, 129, 255, 257, r.randint(1, 600)])
+        lens = [r.choice([0, Nk, r.randint(0, Nk)]) for _ in range(Bk)] if r.random() < 0.6 else None
+        mask = r.choice([None, None, 0.5, 0.95])
+        out.append((Bk * r.choice([1, 2, 3]), Bk, Hk * r.choice([1, 2, 4]), Hk, Nq, Nk, r.choice([64, 128]), lens, mask,
+                    r.random() < 0.5))
+    return out
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("i", range(24))
+def test_cross_shapes_across_the_rules(i, dtype):
+    B, Bk, Hq, Hk, Nq, Nk, d, lens, mask, packed = rand_cases(24, 77)[i]
+    run_case(B, Bk, Hq, Hk, Nq, Nk, d, dtype, lens, mask, seed=i, packed=packed)
+
+
+def test_cross_full_rounds_and_a_split_last():
+    """More items than SMs: those of the last round are split over keys, the others not."""
+    Q, K, V, _, _ = inputs(2, 2, 40, 40, 512, 1100, 64, torch.bfloat16, 12)  # 160 pairs of row tiles
+    O, lse = avq.avq_cross_attention(Q, K, V, lse=True)
+    assert avq.last_kernels() == "cross_tc cross_join"
+    want = ref.cross(Q, K, V)
+    ref.check("O", O, want["O"], want["O_tol"])
+    ref.check("lse", lse, want["lse"], want["lse_tol"])
+    again = avq.avq_cross_attention(Q, K, V)[0]
+    assert torch.equal(again, O)
+
+
+def test_cross_offsets_past_32_bits():
+    """One token over encoder states of more than 2^32 bytes each and 2^31 elements."""
+    Nk, d = (1 << 25) + 4097, 64  # 2^31 elements and more in K and in V
+    kv = torch.zeros((1, Nk, 2, 1, d), dtype=torch.bfloat16, device="cuda")
+    K, V = kv[:, :, 0].transpose(1, 2), kv[:, :, 1].transpose(1, 2)
+    Q = torch.zeros((1, 2, 1, d), dtype=torch.bfloat16, device="cuda")
+    Q[..., 0] = 16.0
+    # keys behind the 2^31st element carry all the weight: logits of 16 against 0
+    far = [Nk - 1, Nk - 4000, (1 << 25) + 5]
+    for i, j in enumerate(far):
+        K[0, 0, j, 0] = 16.0
+        V[0, 0, j, i] = 1.0
+    O, lse = avq.avq_cross_attention(Q, K, V, scale=1.0 / 8, lse=True)  # e^32 against Nk ones
+    e = torch.tensor(32.0, dtype=torch.float64).exp()
+    z = 3 * e + (Nk - 3)
+    want = torch.zeros(1, 2, 1, d, dtype=torch.float64)
+    want[..., :3] = e / z
+    ref.check("O", O, want, 2 * 2.0 ** -8 * want.abs() + 2e-4 * want.abs() + 1e-30)
+    ref.check("lse", lse, torch.full((1, 2, 1), z.log().item(), dtype=torch.float64), torch.full((1, 2, 1), 3e-4))
+
+
+def test_layer_as_it_is_used():
+    """A layer's run: joint projection -> norm and rotation -> quantised self attention, and attention over
+    text states, with the gradients back to the projection, each step against its definition."""
+    g = torch.Generator().manual_seed(21)
+    B, H, N, d, Nt = 2, 4, 784, 64, 77
+    qkv = torch.randn(B, N, 3, H, d, generator=g).bfloat16().cuda()
+    q, k, v = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    text = torch.randn(B, Nt, 2, H, d, generator=g).bfloat16().cuda()
+    tk, tv = text[:, :, 0].transpose(1, 2), text[:, :, 1].transpose(1, 2)
+    lens = torch.tensor([77, 20], dtype=torch.int32).cuda()
+    w = (1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda()
+    t = avq.avq_gilbert_order(28, 28).long()
+    pos = torch.stack([t // 28, t % 28], -1).int()
+    freqs, m = avq.avq_rotary_freqs(64, axes=2, base=100.0)
+    turn = dict(freqs=freqs.cuda(), positions=pos.cuda(), axes=2, mscale=m)
+    Qn, Kn = avq.avq_qk_norm(q, k, w, w, norm="layer", eps=1e-5, **turn)
+    ang = ref.angles(pos, freqs, 2, B, N)
+    for x, y in ((q, Qn), (k, Kn)):
+        want = ref.norm_forward(x.cpu(), w.cpu(), None, "layer", 1e-5, ang, "half", m)
+        ref.check("norm", y, want, ref.row_bound(want, torch.bfloat16))
+    # quantised self attention on the result
+    par = Kn[0, :, ::49].contiguous()  # 16 codewords per head, no children
+    assign, vsum, counts = avq.avq_quantize(Kn, v.contiguous(), par, None)
+    O, _, _ = avq.avq_attention(Qn, par, None, vsum, counts, P=0)
+    P = par.cpu().double()
+    dist = ((P * P).sum(-1)[None, :, None, :] - 2 * Kn.cpu().double() @ P.transpose(-1, -2)[None])
+    got = assign.cpu().long()
+    best = dist.min(-1).values
+    assert (dist.gather(-1, got[..., None])[..., 0] - best <= 1e-5 * (best.abs() + 200)).all()  # nearest, up to near ties
+    onehot = torch.nn.functional.one_hot(got, par.shape[1]).double()
+    vs = onehot.transpose(-1, -2) @ v.cpu().double()
+    n = onehot.sum(2)
+    S = Qn.cpu().double() @ P.transpose(-1, -2)[None] * d ** -0.5
+    E = torch.where(n[:, :, None] > 0, (S - S.amax(-1, keepdim=True)).exp(), torch.zeros_like(S))
+    want = (E @ vs) / (E * n[:, :, None]).sum(-1, keepdim=True)
+    assert (O.cpu().double() - want).abs().max() <= 2e-2 * v.abs().max().item()
+    # text, and back to the projection
+    X, lse = avq.avq_cross_attention(Qn, tk, tv, kv_lens=lens, lse=True)
+    ref_x = ref.cross(Qn, tk, tv, lens.cpu())
+    ref.check("X", X, ref_x["O"], ref_x["O_tol"])
+    dX = torch.randn(B, H, N, d, generator=g).bfloat16().cuda()
+    dQn, dtk, dtv = avq.avq_cross_attention_backward(dX, Qn, tk, tv, X, lse, kv_lens=lens)
+    wb = ref.cross(Qn, tk, tv, lens.cpu(), dO=dX, O_given=X)
+    for name, got_ in (("dQ", dQn), ("dK", dtk), ("dV", dtv)):
+        ref.check(name, got_, wb[name], 2 * wb[name + "_tol"])
+    dq, _, dw, _, _, _ = avq.avq_qk_norm_backward(dQn, None, q, None, w, norm="layer", eps=1e-5, **turn)
+    dx, dww, _ = ref.norm_backward(dQn.cpu(), q.cpu(), w.cpu(), "layer", 1e-5, ang, "half", m)
+    size = dx.abs().amax(-1, keepdim=True) + dQn.cpu().double().abs().amax(-1, keepdim=True) * 8
+    ref.check("dq", dq, dx, ref.row_bound(dx, torch.bfloat16, size))
+    ref.check("dw", dw, dww, 4096 * ref.U32 * dQn.cpu().double().abs().sum((0, 1, 2)) * 8 + 1e-30)
+    avq.avq_check_device()

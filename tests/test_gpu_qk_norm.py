@@ -212,3 +212,68 @@ def test_refuses_overlap_and_wrong_tensors():
         avq.avq_rotary(x, freqs=f.cpu())
     with pytest.raises(avq.AVQError):
         avq.avq_rotary(x, freqs=torch.cat([f, f]))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last heads and tokens are turned like the first."""
+    B, H, N, d = 1, 33, (1 << 20) + 1, 64  # 2.2 billion elements
+    x = torch.zeros((B, H, N, d), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    spots = [(0, 0, 0), (0, H - 1, N - 1), (0, H - 1, 17), (0, 31, N - 2)]
+    rows = [torch.randn(d, generator=g).bfloat16() for _ in spots]
+    for s, r in zip(spots, rows):
+        x[s] = r.cuda()
+    f, _ = avq.avq_rotary_freqs(64)
+    y, _ = avq.avq_rotary(x, freqs=f.cuda())
+    for s, r in zip(spots, rows):
+        want = ref.rotate(r.double()[None, None, None], s[2] * f[None, None, None], "half")[0, 0, 0]
+        ref.check("y", y[s], want, ref.row_bound(want, torch.bfloat16))
+    zero = torch.ones(N, dtype=torch.bool, device="cuda")
+    zero[[17, N - 1]] = False
+    assert (y[0, H - 1, zero] == 0).all() and (y[0, 15] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("seed", range(10))
+def test_shapes_across_the_rules(seed, dtype):
+    """Tokens from one to more than fill the GPU's blocks, heads from one to many, any rotated part."""
+    import random
+
+    r = random.Random(seed)
+    d = r.choice([64, 128])
+    axes = r.choice([1, 2])
+    rot = r.choice([x for x in (0, 16, 32, 48, 64, 80, 96, 112, 128) if x <= d])
+    B, Hq, Hk, N = r.randint(1, 3), r.randint(1, 9), r.randint(0, 5), r.choice([1, 2, 3, 31, 300, 1023, 4700])
+    dt, norm, layout = DT[dtype], r.choice(["rms", "layer"]), r.choice(["half", "interleaved"])
+    g = torch.Generator().manual_seed(seed)
+    Q, K = heads(g, B, Hq, Hk, N, d, dt, r.random() < 0.5)
+    freqs = avq.avq_rotary_freqs(rot, axes=axes, base=1000.0)[0] if rot else None
+    shape = ((B, N) if r.random() < 0.5 else (N,)) + ((2,) if axes == 2 else ())
+    pos = torch.randint(-(1 << 20), 1 << 20, shape, generator=g).int() if rot else None
+    ang = ref.angles(pos, freqs, axes, B, N) if rot else None
+    kw = dict(freqs=None if freqs is None else freqs.cuda(), positions=None if pos is None else pos.cuda(), layout=layout,
+              axes=axes)
+    w = torch.randn(d, generator=g).to(dt).cuda()
+    got = avq.avq_qk_norm(Q, K, w, None, None, w, norm=norm, eps=1e-6, **kw)
+    for x, y, wt, b in ((Q, got[0], w, None), (K, got[1], None, w)):
+        if x is None:
+            continue
+        want = ref.norm_forward(x.cpu(), None if wt is None else wt.cpu(), None if b is None else b.cpu(), norm, 1e-6, ang,
+                                layout, 1.0)
+        ref.check("y", y, want, ref.row_bound(want, dt))
+    dY = [None if x is None else torch.randn(x.shape, generator=g).to(dt).cuda() for x in (Q, K)]
+    out = avq.avq_qk_norm_backward(dY[0], dY[1], Q, K, w, None, norm=norm, eps=1e-6, bias=True, **kw)
+    assert out[3] is None  # no weight was given for the keys
+    for i, x in enumerate((Q, K)):
+        if x is None:
+            continue
+        wt = w.cpu() if i == 0 else None
+        dx, dw, db = ref.norm_backward(dY[i].cpu(), x.cpu(), wt, norm, 1e-6, ang, layout, 1.0)
+        u, rs = ref.normalise(x.cpu().double(), norm, 1e-6)
+        z = dY[i].cpu().double() if ang is None else ref.rotate(dY[i].cpu().double(), ang, layout, 1.0, True)
+        size = rs * (z.abs().amax(-1, keepdim=True) * 8 * (1.0 if wt is None else wt.double().abs().max()))
+        ref.check("dx", out[i], dx, ref.row_bound(dx, dt, size))
+        few = (4096 + d + 64) * ref.U32
+        if i == 0:
+            ref.check("dw", out[2], dw, few * (z.abs().sum((0, 1, 2)) + (z * u).abs().sum((0, 1, 2))) + 1e-30)
+        ref.check("db", out[4 + i], db, few * 2 * z.abs().sum((0, 1, 2)) + 1e-30)
