@@ -505,6 +505,10 @@ def _view(t, name, shape=None, dtype=None, device=None):
 _NO_VIEW = (None, avq_strides(0, 0, 0))
 
 
+def _dense_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _addr(t):
     """Address of a contiguous CUDA tensor, None for None."""
     if t is None:
@@ -585,12 +589,12 @@ def _qk_dims(Q, K, norm, eps, freqs, positions, layout, mscale, axes):
 def _qk_outputs(Q, K, Yq, Yk):
     _expect(Yq, "the queries' output", Q.shape, Q.dtype, Q.device)
     if Yq is None:
-        Yq = Q.new_empty(Q.shape)
+        Yq = _dense_like(Q)
     if K is None:
         return Yq, None
     _expect(Yk, "the keys' output", K.shape, Q.dtype, Q.device)
     if Yk is None:
-        Yk = K.new_empty(K.shape)
+        Yk = _dense_like(K)
     return Yq, Yk
 
 
@@ -668,8 +672,8 @@ def avq_qk_norm_backward(dYq, dYk, Q, K=None, q_weight=None, k_weight=None, norm
     wanted = (q_weight is not None, K is not None and k_weight is not None, bias, bias and K is not None)
     with _Launch(dev, stream) as st:
         dQ, dK = _qk_outputs(Q, K, dQ, dK)
-        sums = torch.empty((4, dims.d), dtype=torch.float32, device=dev)
-        dwq, dwk, dbq, dbk = (sums[i] if w else None for i, w in enumerate(wanted))
+        sums = torch.empty((4, dims.d), dtype=torch.float32, device=dev).unbind(0)
+        dwq, dwk, dbq, dbk = (x if w else None for x, w in zip(sums, wanted))
         if ws is None:
             n = int(lib().avq_qk_norm_workspace_size(ctypes.byref(dims), dt))
             ws = torch.empty(n + 256, dtype=torch.uint8, device=dev)
@@ -725,7 +729,7 @@ def avq_cross_attention(Q, K, V, kv_lens=None, key_mask=None, scale=None, O=None
     dt, dev = _dtype_code(Q), Q.device
     with _Launch(dev, stream) as st:
         if O is None:
-            O = Q.new_empty(Q.shape)
+            O = _dense_like(Q)
         op, os_ = _view(O, "O", Q.shape, Q.dtype, dev)
         if isinstance(lse, torch.Tensor):
             _expect(lse, "lse", Q.shape[:3], torch.float32, dev)
@@ -753,7 +757,7 @@ def avq_cross_attention_backward(dO, Q, K, V, O, lse, kv_lens=None, key_mask=Non
     for t, name, like in ((dQ, "dQ", Q), (dK, "dK", K), (dV, "dV", K)):
         _expect(t, name, like.shape, Q.dtype, dev)
     with _Launch(dev, stream) as st:
-        dQ, dK, dV = (like.new_empty(like.shape) if t is None else t
+        dQ, dK, dV = (_dense_like(like) if t is None else t
                       for t, like in ((dQ, Q), (dK, K), (dV, K)))
         ws, wp, wn = _cross_ws(dims, dt, True, ws, dev)
         _check(lib().avq_cross_attention_backward(
