@@ -24,6 +24,16 @@ __device__ __forceinline__ bool key_seen(const CrossArgs& a, int kb, int j, int 
   return j < count && (a.key_mask == nullptr || __ldg(a.key_mask + (size_t)kb * a.Nk + j) != 0);
 }
 
+// Row r of the rows that read encoder sequence kb and key head kh.
+struct RowAt {
+  int b, h, n;
+};
+__device__ __forceinline__ RowAt row_at(const CrossArgs& a, int kb, int kh, int r) {
+  const int R = a.per_b, G = a.per_h;
+  const int rg = r / a.Nq;
+  return RowAt{kb * R + rg / G, kh * G + rg % G, r % a.Nq};
+}
+
 // Lets a kernel have `bytes` of dynamic shared memory: asked of the runtime once
 // per kernel and device, since small calls are bound by the host.
 template <auto kKernel>

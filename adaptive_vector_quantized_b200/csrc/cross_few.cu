@@ -55,16 +55,6 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Row r of the rows that read encoder sequence kb and key head kh.
-struct RowAt {
-  int b, h, n;
-};
-__device__ __forceinline__ RowAt row_at(const CrossArgs& a, int kb, int kh, int r) {
-  const int R = a.per_b, G = a.per_h;
-  const int rg = r / a.Nq;
-  return RowAt{kb * R + rg / G, kh * G + rg % G, r % a.Nq};
-}
-
 struct Item {
   int kb, kh, chunk, split, count, t0, t1;
 };

@@ -12,10 +12,17 @@
 // Tiles of 64 rows x 64 keys in shared memory as fp32; 256 threads, each 4 x 4
 // scores, in fma.f32x2 (two products an instruction).  All five products read
 // the tiles as they were loaded: rows against rows (S, dO V^T), rows against
-// columns (P V, dS K) and columns against columns (P^T dO, dS^T Q).  Bound by
-// the FMA pipe and, nearly, by shared memory reads (8 16-byte reads for 64
-// products).  Keys that are left out are loaded as zeros, so that infinities
-// and NaN there meet no product.
+// columns (P V, dS K) and columns against columns (P^T dO, dS^T Q).  Keys that
+// are left out are loaded as zeros, so that infinities and NaN there meet no
+// product.
+//
+// Bound by what shared memory hands to registers (32 values a clock and SM, each
+// used by 4 of 128 products a clock: half the FMA pipe's rate) and by the loads,
+// which the other block of the SM covers: K and V (in dQ: V and K) take the same
+// place one after the other, so two blocks fit.  24 heads of 1000 rows and keys of
+// 128: 463 us (26 TFLOP/s; 549 with a place for each, one block an SM), gradients
+// 1.51 ms (1.63).  8 x 4 scores a thread, with half the threads: 511 us and 1.77 ms,
+// as too few warps are left to cover anything.
 #include "cross.cuh"
 #include "fastmath.cuh"
 
@@ -25,40 +32,51 @@ namespace {
 
 constexpr int kT = 64;  // rows and keys of a tile
 constexpr int kThreads = 256;
-constexpr int kPS = kT + 4;  // row pitch of the score tiles
 
-template <int D>
-constexpr int pitch() { return D + 4; }
+// 16-byte piece c of row r of a [64][W] tile: pieces of neighbouring rows lie on
+// different banks
+template <int W>
+__device__ __forceinline__ int place(int r, int c) {
+  return r * W + ((c ^ (r & 7)) << 2);
+}
+template <int W>
+__device__ __forceinline__ float4 get4(const float* tile, int r, int c) {
+  return *reinterpret_cast<const float4*>(tile + place<W>(r, c));
+}
 
-// rows [first, first + 64) of a [.., n, d] tensor; rows outside [0, n) or not wanted are zeros
+// Thread (ty, tx) of 16 x 16 has the rows ty + 16 i (in cols_cols 4 ty + i) and the
+// keys tx + 16 j, or 4 columns of each 64.
+constexpr int kM = 4;
+
+// rows [first, first + 64) of a [.., n, d] tensor; rows that are not wanted are zeros
 template <typename T, int D, typename F>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride, int first, F&& want) {
+#pragma unroll 4
   for (int e = threadIdx.x; e < kT * (D / 4); e += kThreads) {
-    const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+    const int r = e / (D / 4), c = e % (D / 4);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (want(r)) loadE<4>(src + (int64_t)(first + r) * row_stride + c, v);
-    *reinterpret_cast<float4*>(dst + r * pitch<D>() + c) = make_float4(v[0], v[1], v[2], v[3]);
+    if (want(r)) loadE<4>(src + (int64_t)(first + r) * row_stride + 4 * c, v);
+    *reinterpret_cast<float4*>(dst + place<D>(r, c)) = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
 // acc[i][j] = sum_k A[ty + 16 i][k] B[tx + 16 j][k]
 template <int D>
-__device__ __forceinline__ void rows_rows(const float* A, const float* B, int ty, int tx, float acc[4][4]) {
-  float2 s[4][4];
+__device__ __forceinline__ void rows_rows(const float* A, const float* B, int ty, int tx, float acc[][4]) {
+  float2 s[kM][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[i][j] = fm::f2(0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < D; k += 4) {
-    float4 a[4], b[4];
+#pragma unroll 2
+  for (int k = 0; k < D / 4; ++k) {
+    float4 a[kM], b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * pitch<D>() + k);
-      b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * pitch<D>() + k);
-    }
+    for (int i = 0; i < kM; ++i) a[i] = get4<D>(A, ty + 16 * i, k);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) b[j] = get4<D>(B, tx + 16 * j, k);
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s[i][j] = fm::fma2(fm::f2(a[i].x, a[i].y), fm::f2(b[j].x, b[j].y), s[i][j]);
@@ -66,26 +84,29 @@ __device__ __forceinline__ void rows_rows(const float* A, const float* B, int ty
       }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
 }
 
+// A score of the tile: row r, key j
+__device__ __forceinline__ float& score(float* tile, int r, int j) { return tile[place<kT>(r, j >> 2) + (j & 3)]; }
+
 // acc[i][c] += sum_k A[ty + 16 i][k] B[k][4 tx + 64 c ..]  (A: score tile)
 template <int D>
-__device__ __forceinline__ void rows_cols(const float* A, const float* B, int ty, int tx, float2 acc[4][D / 32]) {
+__device__ __forceinline__ void rows_cols(const float* A, const float* B, int ty, int tx, float2 acc[][D / 32]) {
 #pragma unroll 2
-  for (int k = 0; k < kT; k += 4) {
-    float4 a[4];
+  for (int k = 0; k < kT / 4; ++k) {
+    float4 a[kM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * kPS + k);
+    for (int i = 0; i < kM; ++i) a[i] = get4<kT>(A, ty + 16 * i, k);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(B + (k + kk) * pitch<D>() + 4 * tx + 64 * c);
+        const float4 v = get4<D>(B, 4 * k + kk, tx + 16 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kM; ++i) {
           const float x = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
           acc[i][2 * c] = fm::fma2(fm::f2(x, x), fm::f2(v.x, v.y), acc[i][2 * c]);
           acc[i][2 * c + 1] = fm::fma2(fm::f2(x, x), fm::f2(v.z, v.w), acc[i][2 * c + 1]);
@@ -95,40 +116,39 @@ __device__ __forceinline__ void rows_cols(const float* A, const float* B, int ty
   }
 }
 
-// acc[i][c] += sum_k A[k][4 ty + i] B[k][4 tx + 64 c ..]  (A: score tile)
+// acc[i][c] += sum_k A[k][kM ty + i] B[k][4 tx + 64 c ..]  (A: score tile)
 template <int D>
-__device__ __forceinline__ void cols_cols(const float* A, const float* B, int ty, int tx, float2 acc[4][D / 32]) {
+__device__ __forceinline__ void cols_cols(const float* A, const float* B, int ty, int tx, float2 acc[][D / 32]) {
 #pragma unroll 4
   for (int k = 0; k < kT; ++k) {
-    const float4 a = *reinterpret_cast<const float4*>(A + k * kPS + 4 * ty);
-    const float av[4] = {a.x, a.y, a.z, a.w};
+    const float4 a = get4<kT>(A, k, ty);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const float4 v = *reinterpret_cast<const float4*>(B + k * pitch<D>() + 4 * tx + 64 * c);
+      const float4 v = get4<D>(B, k, tx + 16 * c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i][2 * c] = fm::fma2(fm::f2(av[i], av[i]), fm::f2(v.x, v.y), acc[i][2 * c]);
-        acc[i][2 * c + 1] = fm::fma2(fm::f2(av[i], av[i]), fm::f2(v.z, v.w), acc[i][2 * c + 1]);
+      for (int i = 0; i < kM; ++i) {
+        const float x = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : a.w;
+        acc[i][2 * c] = fm::fma2(fm::f2(x, x), fm::f2(v.x, v.y), acc[i][2 * c]);
+        acc[i][2 * c + 1] = fm::fma2(fm::f2(x, x), fm::f2(v.z, v.w), acc[i][2 * c + 1]);
       }
     }
   }
 }
 
-template <int D>
-__device__ __forceinline__ void clear(float2 acc[4][D / 32]) {
+template <int C>
+__device__ __forceinline__ void clear(float2 (&acc)[kM][C]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kM; ++i)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[i][c] = fm::f2(0.f, 0.f);
+    for (int c = 0; c < C; ++c) acc[i][c] = fm::f2(0.f, 0.f);
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_simt_kernel(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) cross_simt_kernel(const CrossArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
-  float* sK = sQ + kT * pitch<D>();
-  float* sV = sK + kT * pitch<D>();
-  float* sP = sV + kT * pitch<D>();
+  float* sKV = sQ + kT * D;  // K, then V
+  float* sP = sKV + kT * D;
   __shared__ unsigned char seen[kT];
   const int tiles = (a.Nq + kT - 1) / kT;
   const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
@@ -144,23 +164,24 @@ __global__ void __launch_bounds__(kThreads) cross_simt_kernel(const CrossArgs a)
   const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
   load_tile<T, D>(sQ, Q, a.qs.n, row0, [&](int r) { return row0 + r < a.Nq; });
   const float c2 = a.scale * kLog2e;
-  float m[4], z[4];
-  float2 o[4][D / 32];
-  clear<D>(o);
+  float m[kM], z[kM];
+  float2 o[kM][D / 32];
+  clear(o);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, z[i] = 0.f;
+  for (int i = 0; i < kM; ++i) m[i] = -INFINITY, z[i] = 0.f;
   for (int t = t0; t < t1; ++t) {
     const int k0 = t * kT;
     __syncthreads();  // the tiles below are still read by the last trip
     if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
     __syncthreads();
-    load_tile<T, D>(sK, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
-    load_tile<T, D>(sV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
+    load_tile<T, D>(sKV, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
     __syncthreads();
-    float s[4][4];
-    rows_rows<D>(sQ, sK, ty, tx, s);
+    float s[kM][4];
+    rows_rows<D>(sQ, sKV, ty, tx, s);
+    __syncthreads();
+    load_tile<T, D>(sKV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kM; ++i) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -172,25 +193,26 @@ __global__ void __launch_bounds__(kThreads) cross_simt_kernel(const CrossArgs a)
       const float mn = fmaxf(m[i], top);
       const float base = mn == -INFINITY ? 0.f : mn * c2;
       const float keep = m[i] == -INFINITY ? 0.f : exp2f(m[i] * c2 - base);
-      float sum = 0.f;
+      z[i] *= keep;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s[i][j] = exp2f(fmaf(s[i][j], c2, -base));
-        sum += s[i][j];
-        sP[(ty + 16 * i) * kPS + tx + 16 * j] = s[i][j];
+        z[i] += s[i][j];
+        score(sP, ty + 16 * i, tx + 16 * j) = s[i][j];
       }
-#pragma unroll
-      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      z[i] = z[i] * keep + sum;
       m[i] = mn;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) o[i][c] = fm::mul2(o[i][c], fm::f2(keep, keep));
     }
     __syncthreads();
-    rows_cols<D>(sP, sV, ty, tx, o);
+    rows_cols<D>(sP, sKV, ty, tx, o);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) z[i] += __shfl_xor_sync(0xffffffffu, z[i], w);
+#pragma unroll
+  for (int i = 0; i < kM; ++i) {
     const int r = row0 + ty + 16 * i;
     if (r >= a.Nq) continue;
     const float inv = z[i] > 0.f ? 1.f / z[i] : (z[i] == 0.f ? 0.f : z[i]);  // NaN stays NaN
@@ -213,15 +235,11 @@ __global__ void __launch_bounds__(kThreads) cross_simt_kernel(const CrossArgs a)
   }
 }
 
-// P and dS of one tile pair: rows ty + 16 i of the row tile, keys tx + 16 j.
-template <int D>
-__device__ __forceinline__ void scores_back(const float* sQ, const float* sG, const float* sK, const float* sV,
-                                            const float* sL, const float* sDelta, const unsigned char* seen, int ty,
-                                            int tx, float c2, float scale, float p[4][4], float ds[4][4]) {
-  rows_rows<D>(sQ, sK, ty, tx, p);
-  rows_rows<D>(sG, sV, ty, tx, ds);
+// From Q K^T and dO V^T of a tile pair: P and dS of the rows ty + 16 i, keys tx + 16 j.
+__device__ __forceinline__ void scores_back(const float* sL, const float* sDelta, const unsigned char* seen, int ty,
+                                            int tx, float c2, float scale, float p[][4], float ds[][4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kM; ++i) {
     const float l = sL[ty + 16 * i], dl = sDelta[ty + 16 * i];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -242,14 +260,14 @@ __device__ __forceinline__ void load_rows(const CrossArgs& a, float* sL, float* 
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kernel(const CrossArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
-  float* sV = sK + kT * pitch<D>();
-  float* sQ = sV + kT * pitch<D>();
-  float* sG = sQ + kT * pitch<D>();
-  float* sP = sG + kT * pitch<D>();
-  float* sD = sP + kT * kPS;
+  float* sV = sK + kT * D;
+  float* sQ = sV + kT * D;
+  float* sG = sQ + kT * D;
+  float* sP = sG + kT * D;
+  float* sD = sP + kT * kT;
   __shared__ float sL[kT], sDelta[kT];
   __shared__ unsigned char seen[kT];
   const int tiles = (a.Nk + kT - 1) / kT;
@@ -266,9 +284,9 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArg
   load_tile<T, D>(sV, static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h, a.vs.n, k0,
                   [&](int r) { return seen[r] != 0; });
   const float c2 = a.scale * kLog2e;
-  float2 dk[4][D / 32], dv[4][D / 32];
-  clear<D>(dk);
-  clear<D>(dv);
+  float2 dk[kM][D / 32], dv[kM][D / 32];
+  clear(dk);
+  clear(dv);
   const int rtiles = (a.Nq + kT - 1) / kT;
   const int all = R * G * rtiles;
   const int i0 = part_begin(all, split, a.splits), i1 = k0 < count ? part_begin(all, split + 1, a.splits) : i0;
@@ -282,14 +300,16 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArg
                     [&](int r) { return row0 + r < a.Nq; });
     load_rows(a, sL, sDelta, ((size_t)b * a.Hq + h) * a.Nq, row0);
     __syncthreads();
-    float p[4][4], ds[4][4];
-    scores_back<D>(sQ, sG, sK, sV, sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
+    float p[kM][4], ds[kM][4];
+    rows_rows<D>(sQ, sK, ty, tx, p);
+    rows_rows<D>(sG, sV, ty, tx, ds);
+    scores_back(sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sP[(ty + 16 * i) * kPS + tx + 16 * j] = p[i][j];
-        sD[(ty + 16 * i) * kPS + tx + 16 * j] = ds[i][j];
+        score(sP, ty + 16 * i, tx + 16 * j) = p[i][j];
+        score(sD, ty + 16 * i, tx + 16 * j) = ds[i][j];
       }
     __syncthreads();
     cols_cols<D>(sP, sG, ty, tx, dv);
@@ -297,8 +317,8 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArg
   }
   const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = k0 + 4 * ty + i;
+  for (int i = 0; i < kM; ++i) {
+    const int r = k0 + kM * ty + i;
     if (r >= a.Nk) continue;
     const size_t at = (((size_t)kb * a.Hk + kh) * a.Nk + r) * D;
 #pragma unroll
@@ -317,13 +337,12 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dkv_kernel(const CrossArg
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_simt_dq_kernel(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float* sK = sm;
-  float* sV = sK + kT * pitch<D>();
-  float* sQ = sV + kT * pitch<D>();
-  float* sG = sQ + kT * pitch<D>();
-  float* sD = sG + kT * pitch<D>();
+  float* sKV = sm;  // V, then K
+  float* sQ = sKV + kT * D;
+  float* sG = sQ + kT * D;
+  float* sD = sG + kT * D;
   __shared__ float sL[kT], sDelta[kT];
   __shared__ unsigned char seen[kT];
   const int tiles = (a.Nq + kT - 1) / kT;
@@ -344,27 +363,31 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dq_kernel(const CrossArgs
   const T* K = static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h;
   const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
   const float c2 = a.scale * kLog2e;
-  float2 dq[4][D / 32];
-  clear<D>(dq);
+  float2 dq[kM][D / 32];
+  clear(dq);
   for (int t = t0; t < t1; ++t) {
     const int k0 = t * kT;
     __syncthreads();
     if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
     __syncthreads();
-    load_tile<T, D>(sK, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
-    load_tile<T, D>(sV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
+    load_tile<T, D>(sKV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
     __syncthreads();
-    float p[4][4], ds[4][4];
-    scores_back<D>(sQ, sG, sK, sV, sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sD[(ty + 16 * i) * kPS + tx + 16 * j] = ds[i][j];
+    float p[kM][4], ds[kM][4];
+    rows_rows<D>(sG, sKV, ty, tx, ds);
     __syncthreads();
-    rows_cols<D>(sD, sK, ty, tx, dq);
+    load_tile<T, D>(sKV, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
+    __syncthreads();
+    rows_rows<D>(sQ, sKV, ty, tx, p);
+    scores_back(sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) score(sD, ty + 16 * i, tx + 16 * j) = ds[i][j];
+    __syncthreads();
+    rows_cols<D>(sD, sKV, ty, tx, dq);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kM; ++i) {
     const int r = row0 + ty + 16 * i;
     if (r >= a.Nq) continue;
 #pragma unroll
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) cross_simt_dq_kernel(const CrossArgs
 
 template <typename T, int D>
 cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(3 * kT * pitch<D>() + kT * kPS) * sizeof(float);
+  const size_t smem = (size_t)(2 * kT * D + kT * kT) * sizeof(float);
   cudaError_t e = allow_smem<cross_simt_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
@@ -390,7 +413,7 @@ cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
 }
 template <typename T, int D>
 cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(4 * kT * pitch<D>() + 2 * kT * kPS) * sizeof(float);
+  const size_t smem = (size_t)(4 * kT * D + 2 * kT * kT) * sizeof(float);
   cudaError_t e = allow_smem<cross_simt_dkv_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT)), a.splits);
@@ -399,7 +422,7 @@ cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
 }
 template <typename T, int D>
 cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(4 * kT * pitch<D>() + kT * kPS) * sizeof(float);
+  const size_t smem = (size_t)(3 * kT * D + kT * kT) * sizeof(float);
   cudaError_t e = allow_smem<cross_simt_dq_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);

@@ -175,11 +175,31 @@ int split_count(long long items, long long units, long long target) {
 }
 long long tiles64(long long n) { return (n + 63) / 64; }
 
+// Parts for the items of the CUDA-core kernels, each a walk over `units` tiles, on
+// `slots` resident blocks: as many as make the rounds shortest, where a part costs
+// about half a tile more (its own tile's load, its result's way to memory and back).
+// 12 heads of 1001 rows over 333 keys of 64 (192 items of up to 6 tiles): 45 us, 55 with
+// as many parts as the slots hold at once.
+int even_split(long long items, long long units, long long slots) {
+  int best = 1;
+  double least = 0;
+  for (int n = 1; n <= 64 && (n == 1 || n <= units); ++n) {
+    const double cost = (double)((items * n + slots - 1) / slots) * ((double)((units + n - 1) / n) + 0.5);
+    if (n == 1 || cost < least) best = n, least = cost;
+  }
+  return best;
+}
+
 // Rows per key head up to which mma.sync on 16 rows at a time beats the 128-row
 // tiles of tcgen05: with 32 sequences of 4096 keys, 8 key heads, 16 rows take 53
 // against 93 us at d = 64 and 91 against 99 at d = 128, 32 rows 78 against 93 and
 // 125 against 99.
 constexpr long long few_rows(int d) { return d == 64 ? 32 : 16; }
+
+// The same for 32-bit inputs, four rows at a time against 64-row tiles: 8 sequences of
+// 4096 keys, 8 heads, 8 rows take 46 against 182 us at d = 64 and 63 against 346 at
+// d = 128, 32 rows 182 against 182 and 259 against 348, 48 rows 218 against 183 at d = 64.
+constexpr long long kFewRowsF32 = 32;
 
 // How the items of a kernel with one block per SM, each a walk over `units` key
 // tiles, fill its rounds: the items of full rounds stay whole, those of the last
@@ -219,14 +239,14 @@ struct CrossPlan {
 
 CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   CrossPlan p;
-  const long long target = 2ll * num_sms();
+  const long long slots = 2ll * num_sms();  // blocks of the CUDA-core kernels
   const long long rows = (long long)s.B * s.Hq * s.Nq, keys = (long long)s.Bk * s.Hk * s.Nk;
   const long long row_items = (long long)s.B * s.Hq * tiles64(s.Nq), key_items = (long long)s.Bk * s.Hk * tiles64(s.Nk);
   const long long shared = (long long)(s.B / s.Bk) * (s.Hq / s.Hk);  // query heads that read one key head
   const long long key_tiles = (s.Nk + 127) / 128;
   p.tc = dt == AVQ_BF16 && api_path() != AVQ_PATH_SIMT && s.Nk > 0;
   if (!backward) {
-    p.few = p.tc && shared * s.Nq <= few_rows(s.d);
+    p.few = p.tc ? shared * s.Nq <= few_rows(s.d) : dt == AVQ_F32 && shared * s.Nq <= kFewRowsF32;
     if (p.tc && !p.few) {  // pairs of 128-row tiles
       p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 255) / 256), key_tiles);
       p.part = up256((size_t)p.rounds.parts * 256 * s.d * 4);
@@ -235,8 +255,13 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
     }
     // few: two rounds of the resident blocks, since lengths differ (32 sequences
     // of 4096 to 8191 keys took 68 us with 1 or 2 rounds, 71 with 4, 78 with 8)
-    p.splits = p.few ? split_count((long long)s.Bk * s.Hk * ((shared * s.Nq + 15) / 16), s.Nk / 128, 4ll * num_sms())
-                     : split_count(row_items, tiles64(s.Nk), target);
+    const long long pairs = (long long)s.Bk * s.Hk;
+    if (!p.few)
+      p.splits = even_split(row_items, tiles64(s.Nk), slots);
+    else if (p.tc)
+      p.splits = split_count(pairs * ((shared * s.Nq + 15) / 16), s.Nk / 128, 4ll * num_sms());
+    else
+      p.splits = split_count(pairs * ((shared * s.Nq + 3) / 4), s.Nk / 64, 6ll * num_sms());
     if (p.splits > 1) {
       p.part = up256((size_t)p.splits * rows * s.d * 4);
       p.part_lse = up256((size_t)p.splits * rows * 4);
@@ -251,9 +276,9 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
     dq = (size_t)p.rounds.parts * 128 * s.d * 4;
     p.dkv_splits = split_count((long long)s.Bk * s.Hk * key_tiles, shared * ((s.Nq + 127) / 128), num_sms());
   } else {
-    p.dq_splits = split_count(row_items, tiles64(s.Nk), target);
+    p.dq_splits = even_split(row_items, tiles64(s.Nk), slots);
     dq = p.dq_splits > 1 ? (size_t)p.dq_splits * rows * s.d * 4 : 0;
-    if (key_items > 0) p.dkv_splits = split_count(key_items, shared * tiles64(s.Nq), target);
+    if (key_items > 0) p.dkv_splits = even_split(key_items, shared * tiles64(s.Nq), s.d == 64 ? slots : slots / 2);
   }
   const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * keys * s.d * 4 : 0;
   p.part = up256(dq > dkv ? dq : dkv);
@@ -418,7 +443,7 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
     if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");
     e = p.few ? launch_cross_few(a, err, cs, log) : launch_cross_tc(a, err, cs, log);
   } else {
-    e = launch_cross_simt(a, dtype, cs, log);
+    e = p.few ? launch_cross_few_f32(a, cs, log) : launch_cross_simt(a, dtype, cs, log);
   }
   if (e == cudaSuccess && !items && a.splits > 1) e = launch_cross_join(a, dtype, cs, log);
   return api_finish(e, "cross attention launch", log);

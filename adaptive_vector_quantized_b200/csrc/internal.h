@@ -149,6 +149,7 @@ struct CrossArgs {
   const int32_t* kv_lens;
   const uint8_t* key_mask;
 };
+cudaError_t launch_cross_few_f32(const CrossArgs& a, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_simt(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_simt_dkv(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_simt_dq(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);

@@ -390,3 +390,38 @@ def test_layer_as_it_is_used():
     ref.check("dq", dq, dx, ref.row_bound(dx, torch.bfloat16, size))
     ref.check("dw", dw, dww, 4096 * ref.U32 * dQn.cpu().double().abs().sum((0, 1, 2)) * 8 + 1e-30)
     avq.avq_check_device()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dims, lens, mask", [
+    ((2, 2, 4, 4, 1, 1), None, None),
+    ((4, 2, 6, 2, 1, 15), [15, 1], None),
+    ((2, 2, 8, 1, 4, 17), [0, 17], None),
+    ((1, 1, 2, 2, 31, 2049), None, 0.5),
+    ((6, 1, 5, 1, 1, 4100), [4099], 0.02),
+    ((3, 3, 2, 2, 32, 700), [700, 63, 0], None),
+    ((1, 1, 2, 2, 33, 700), [64], None),
+])
+def test_cross_f32_few_rows(dims, lens, mask, d):
+    B, Bk, Hq, Hk, Nq, Nk = dims
+    kernels = run_case(B, Bk, Hq, Hk, Nq, Nk, d, "f32", lens, mask, packed=B % 2 == 0)
+    assert ("cross_few_f32" in kernels) == (B // Bk * (Hq // Hk) * Nq <= 32)
+
+
+def test_cross_f32_few_rows_captured():
+    Q, K, V, _, _ = inputs(2, 2, 4, 2, 1, 3333, 128, torch.float32)
+    want, _ = avq.avq_cross_attention(Q, K, V)
+    O = torch.empty_like(want)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        avq.avq_cross_attention(Q, K, V, O=O)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        avq.avq_cross_attention(Q, K, V, O=O)
+    V.neg_()
+    O.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(O, -want)
