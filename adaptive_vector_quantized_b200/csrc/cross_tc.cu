@@ -15,7 +15,8 @@
 // steps of 128 keys S would have to wait for P V of the same tile (TMEM has no
 // room for a second buffer at d = 128); 16384 x 16384, 8 heads of 128: 1.36 ms
 // like that, 1.03 ms in halves, although a product with 64 columns takes 48
-// clocks of shared memory reads instead of 32.
+// clocks of shared memory reads instead of 32.  With the last round's items split
+// over the keys 0.90 ms (1.22 PFLOP/s).
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the scale in use (P then stays below 2^8, and its rounding to bf16

@@ -17,16 +17,20 @@
 //   dQ:     S(j), S(j+1) in turn              dP(j) -> dS(j) -> dQ(j), dP(j+1)
 // For dK and dV the chains run apart for the two groups' halves of a tile, so
 // that one group works while the MMAs of the other's half do (8192 rows x 4096
-// keys, 8 heads of 128 on 4: 298 us against 312); for dQ, whose S is a step ahead
-// anyhow, whole tiles are better (233 us against 246): a product with 64 columns
-// takes 48 clocks of shared memory reads, one with 128 takes 64.
+// keys, 8 heads of 128 on 4: 298 us against 312 when both were built); for dQ, whose
+// S is a step ahead anyhow, whole tiles are better (233 us against 246): a product
+// with 64 columns takes 48 clocks of shared memory reads, one with 128 takes 64.
+// What bound both most was the MMA warps' own issue: run converged, with their
+// descriptors in uniform registers, they brought the whole call from 463 to 394 us
+// (875 TFLOP/s of the 5 products that the formulas need).
 #include "cross_tc.cuh"
 
 //
 // With at most one key tile (text states) and d = 64 the dK/dV blocks see every
 // key of a row, and TMEM has room: they form dQ too, from a copy of dS in shared
 // memory (the rows of dS^T are keys, so it is read column by column), and Q and
-// dO are read once: 24 heads of 4096 rows over 77 keys 65 us apart, 39 us so.
+// dO are read once: 24 heads of 4096 rows over 77 keys 65 us apart, 39 us so,
+// 32 us with the converged MMA warps.
 
 namespace avq {
 

@@ -504,12 +504,15 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const float* part, int
 
 int groups_of(int d) { return kThreads / (d / 8); }
 
-// Tokens per tile: as many as fit the block's lane groups (sine and cosine
-// are then shared by the token's heads alone), fewer while the tiles would
-// leave SMs idle; the freed groups share the token's heads.
+// Tokens per tile (forward): as many as fit the block's lane groups (sine and
+// cosine are then shared by the token's heads alone), fewer while the tiles would
+// leave SMs idle; the freed groups share the token's heads.  12 heads of 64: 784
+// tokens 5.6 us, 8.0 with whole tiles, 6.9 with two tiles an SM; 2048 tokens 6.1,
+// 8.1, 9.2.  The gradients take whole tiles: 300 tokens of 8 heads of 128 8.2 us,
+// 8.9 with a tile an SM, 1568 tokens 11.3 and 12.2 (each block adds its own sums).
 int tile_tokens(int d, int tokens) {
   int tb = groups_of(d);
-  while (tb > 1 && (tokens + tb - 1) / tb < 2 * num_sms()) tb >>= 1;
+  while (tb > 1 && (tokens + tb - 1) / tb < num_sms()) tb >>= 1;
   return tb;
 }
 
@@ -561,7 +564,7 @@ void launch_bwd_norm(const Params& p, int norm, bool half, int tiles, dim3 grid,
 
 int backward_blocks(const avq_qk_dims& s) {
   const int tokens = s.B * s.N;
-  const int tb = tile_tokens(s.d, tokens);
+  const int tb = groups_of(s.d);
   const int tiles = (tokens + tb - 1) / tb;
   const int most = s.Hk > 0 ? num_sms() : 2 * num_sms();  // the two blocks that an SM holds
   return tiles < most ? tiles : most;
@@ -599,6 +602,7 @@ cudaError_t launch_qk_norm_backward(const avq_qk_dims& s, avq_dtype dt, const vo
   Params p = params_of(s, xs, pos, freqs);
   for (int i = 0; i < 2; ++i) p.x[i] = x[i], p.w[i] = w[i], p.g[i] = g[i], p.gs[i] = gs[i], p.y[i] = dx[i];
   p.sign = -1.f;
+  p.tb = groups_of(s.d);
   p.part = static_cast<float*>(ws);
   const int tiles = (p.tokens + p.tb - 1) / p.tb;
   const bool half = s.layout == AVQ_ROTARY_HALF;
