@@ -43,9 +43,15 @@ avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, 
       return api_fail(AVQ_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", name);
     if (use == kCopied && i == 2 && N > 1 && v[i] == 0)
       return api_fail(AVQ_ERR_INVALID_ARG, "%s: tokens must not repeat (stride 0)", name);
-    if (use == kWritten && n[i] > 1 && v[i] < d)
-      return api_fail(AVQ_ERR_INVALID_ARG, "%s: an output's heads must not overlap", name);
     last += v[i] * (int64_t)(n[i] > 0 ? n[i] - 1 : 0);
+  }
+  // of what is written, each dimension steps over what those with shorter strides span
+  for (int i = 0; i < 3 && use == kWritten; ++i) {
+    int64_t inner = d;
+    for (int j = 0; j < 3; ++j)
+      if (j != i && n[j] > 1 && (v[j] < v[i] || (v[j] == v[i] && j < i))) inner += v[j] * (int64_t)(n[j] - 1);
+    if (n[i] > 1 && v[i] < inner)
+      return api_fail(AVQ_ERR_INVALID_ARG, "%s: an output's rows must not overlap", name);
   }
   *out = Strides{v[0], v[1], v[2]};
   if (span != nullptr) *span = (size_t)(last * es);
@@ -422,6 +428,13 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   for (int i = 0; i < 3; ++i)
     if (spans[i] > 0 && overlap(O, ospan, ins[i], spans[i])) return api_fail(AVQ_ERR_INVALID_ARG, "O overlaps an input");
   AVQ_TRY(optional_vector(lse, "lse"));
+  if (lse != nullptr) {
+    const size_t n = (size_t)s.B * s.Hq * s.Nq * sizeof(float);
+    for (int i = 0; i < 3; ++i)
+      if (spans[i] > 0 && overlap(lse, n, ins[i], spans[i]))
+        return api_fail(AVQ_ERR_INVALID_ARG, "lse overlaps an input");
+    if (overlap(lse, n, O, ospan)) return api_fail(AVQ_ERR_INVALID_ARG, "lse overlaps O");
+  }
   const CrossPlan p = plan_cross(s, dtype, false);
   AVQ_TRY(check_ws(p.total(), ws, ws_bytes));
   if (api_path() == AVQ_PATH_TC && dtype != AVQ_BF16)
@@ -459,7 +472,7 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   AVQ_TRY(check_cross(dims, dtype));
   const avq_cross_dims& s = *dims;
   CrossArgs a{};
-  size_t spans[5];
+  size_t spans[6];
   AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
   AVQ_TRY(need_ptr(dO, "dO"));
   AVQ_TRY(view(do_strides, s.B, s.Hq, s.Nq, s.d, dtype, kCopied, "dO", &a.gs, &spans[3]));
@@ -472,11 +485,12 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
     AVQ_TRY(need_ptr(dV, "dV"));
   }
   const size_t qn = (size_t)s.B * s.Hq * s.Nq * s.d, kn = (size_t)s.Bk * s.Hk * s.Nk * s.d;
-  const void* ins[5] = {Q, K, V, dO, O};
+  const void* ins[6] = {Q, K, V, dO, O, lse};
+  spans[5] = (size_t)s.B * s.Hq * s.Nq * sizeof(float);
   const void* outs[3] = {dQ, dK, dV};
   const size_t bytes[3] = {qn * elem(dtype), kn * elem(dtype), kn * elem(dtype)};
   for (int o = 0; o < (s.Nk > 0 ? 3 : 1); ++o) {
-    for (int i = 0; i < 5; ++i)
+    for (int i = 0; i < 6; ++i)
       if (spans[i] > 0 && overlap(outs[o], bytes[o], ins[i], spans[i]))
         return api_fail(AVQ_ERR_INVALID_ARG, "a gradient overlaps an input");
     for (int i = 0; i < o; ++i)

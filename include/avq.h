@@ -457,7 +457,8 @@ typedef struct {
  * matter, infinities and NaN included.  A row with no key gives O = 0 and
  * lse = -inf.
  * Outputs (device): O [B,Hq,Nq,d] of `dtype` with strides; lse fp32
- * [B,Hq,Nq], dense, or NULL.  O overlaps no input.
+ * [B,Hq,Nq], dense, or NULL.  O and lse overlap no input and not each other;
+ * O's strides let no two rows overlap.
  * Workspace: avq_cross_workspace_size(dims, dtype, 0) bytes, 256-byte
  * aligned; NULL when that is 0.  It depends on the kernel family
  * (avq_set_path) in force, as the call does.

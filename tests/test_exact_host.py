@@ -117,10 +117,10 @@ def test_cross_attention_workspace_is_checked():
     for dims, dt in ((cd(Nk=20000), avq.AVQ_BF16), (cd(Nk=20000), avq.AVQ_F32), (cd(Nq=300, Nk=20000), avq.AVQ_BF16)):
         need = L.avq_cross_workspace_size(P(dims), dt, 0)
         assert need > 0 and need % 256 == 0  # few rows, many keys: split
-        ks = dense(2, 2, 20000, 64)
-        assert cross(dims, dt, ks=ks, ws=None, n=0) == avq.AVQ_ERR_WORKSPACE
-        assert cross(dims, dt, ks=ks, n=need - 1) == avq.AVQ_ERR_WORKSPACE
-        assert cross(dims, dt, ks=ks, ws=FAKE[9] + 16) == BAD
+        ks, qs = dense(2, 2, 20000, 64), dense(2, 4, dims.Nq, 64)
+        assert cross(dims, dt, qs=qs, os_=qs, ks=ks, ws=None, n=0) == avq.AVQ_ERR_WORKSPACE
+        assert cross(dims, dt, qs=qs, os_=qs, ks=ks, n=need - 1) == avq.AVQ_ERR_WORKSPACE
+        assert cross(dims, dt, qs=qs, os_=qs, ks=ks, ws=FAKE[9] + 16) == BAD
     assert L.avq_cross_workspace_size(P(cd(B=3)), avq.AVQ_BF16, 0) == 0
 
 
@@ -198,3 +198,17 @@ def test_rotary_freqs():
 def test_rotary_freqs_refuses(kw):
     with pytest.raises(avq.AVQError):
         avq.avq_rotary_freqs(**kw)
+
+
+def test_cross_refuses_outputs_that_overlap_themselves(monkeypatch):
+    S = avq.avq_strides
+    monkeypatch.setenv("AVQ_FAULT", "cross_attention")
+    for st in (S(2560, 640, 64), S(2560, 64, 256), S(64, 1280, 128), S(640, 1280, 64), S(10240, 64, 512)):
+        assert cross(os_=st) == avq.AVQ_ERR_CUDA and "injected" in avq.last_error()  # every order of the dimensions
+    for st in (S(64, 64, 128), S(640, 640, 64), S(2560, 576, 64), S(2560, 64, 192), S(2496, 64, 256), S(32, 640, 64)):
+        assert cross(os_=st) == BAD and "must not overlap" in avq.last_error()
+
+
+def test_cross_refuses_an_lse_inside_another_tensor():
+    for t in (FAKE[0], FAKE[1], FAKE[2], FAKE[3] + 64):
+        assert cross(lse=t) == BAD and "lse overlaps" in avq.last_error()

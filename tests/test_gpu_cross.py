@@ -401,6 +401,7 @@ def test_layer_as_it_is_used():
     ((6, 1, 5, 1, 1, 4100), [4099], 0.02),
     ((3, 3, 2, 2, 32, 700), [700, 63, 0], None),
     ((1, 1, 2, 2, 33, 700), [64], None),
+    ((2, 2, 4, 2, 3, 0), None, None),
 ])
 def test_cross_f32_few_rows(dims, lens, mask, d):
     B, Bk, Hq, Hk, Nq, Nk = dims
