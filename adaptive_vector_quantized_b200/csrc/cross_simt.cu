@@ -261,6 +261,7 @@ __device__ __forceinline__ void load_rows(const CrossArgs& a, float* sL, float* 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kernel(const CrossArgs a) {
+  allow_dependents();  // dQ's blocks may take the places that these leave
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
   float* sV = sK + kT * D;
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
         put4(static_cast<T*>(a.dQ) + at, v);
     }
   }
+  grid_dependency_wait();  // whatever comes after this kernel comes after dK's and dV's too
 }
 
 template <typename T, int D>
@@ -426,8 +428,8 @@ cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
   cudaError_t e = allow_smem<cross_simt_dq_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
-  cross_simt_dq_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  // dK and dV's kernel started after delta was complete and writes nothing that is read here
+  return launch_after(cross_simt_dq_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
 }
 
 }  // namespace

@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
   __syncthreads();
   tc::tc_fence_after();
   grid_dependency_wait();  // delta
+  allow_dependents();      // dQ's blocks may take the SMs that these leave
   const Guard guard{err, sAbort};
   const uint32_t tmem = *sTmem;
   // S | dP | dV | dK, and behind them dQ of even and of odd steps
@@ -641,6 +642,7 @@ __device__ __forceinline__ RowItem row_item(const CrossArgs& a, int i, int rtile
   return x;
 }
 
+// Starts beside the kernel of dK and dV, on the SMs that it leaves.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_constant__ Maps maps,
                                                                  const CrossArgs a, unsigned int* err, int items,
@@ -649,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
   extern __shared__ __align__(1024) uint8_t sm[];
   if (tc::smem_u32(sm) & 1023u) {  // no room is left to align it here
     if (threadIdx.x == 0) atomicOr(err, kErrInternal);
+    grid_dependency_wait();
     return;
   }
   const Bars bar = bars_of<D>(sm);
@@ -894,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
   tc::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+  grid_dependency_wait();  // whatever comes after this kernel comes after dK's and dV's too
 }
 
 Strides dense(int B, int H, int N, int d) {
@@ -941,8 +945,8 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, Launc
   const int items = a.B * a.Hq * rtiles;
   const int launch = a.whole + (items - a.whole) * a.splits;
   const int grid = launch < num_sms() ? launch : num_sms();
-  cross_tc_dq_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, launch, rtiles);
-  e = cudaGetLastError();
+  // dK and dV's kernel waited for delta and writes nothing that is read here
+  e = launch_after(cross_tc_dq_kernel<D>, dim3(grid), dim3(kThreads), smem, st, m, a, err, launch, rtiles);
   if (e == cudaSuccess && a.whole < items) e = launch_cross_join_items(a, items, rtiles, 128, false, st, log);
   return e;
 }

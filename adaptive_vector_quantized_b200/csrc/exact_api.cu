@@ -240,6 +240,7 @@ struct CrossPlan {
   Rounds rounds;     // tc: forward, or dQ
   int dkv_splits = 1, dq_splits = 1;
   size_t part = 0, part_lse = 0, delta = 0;  // bytes, each a multiple of 256
+  size_t dq_part = 0;                        // where dQ's begin in part
   size_t total() const { return part + part_lse + delta; }
 };
 
@@ -275,7 +276,7 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
     return p;
   }
   p.delta = up256((size_t)rows * 4);
-  // dK and dV, then dQ, one after the other in the same place
+  // dQ may be formed while dK and dV are: each in a place of its own
   size_t dq;
   if (p.tc) {
     p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 127) / 128), key_tiles);
@@ -287,7 +288,8 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
     if (key_items > 0) p.dkv_splits = even_split(key_items, shared * tiles64(s.Nq), s.d == 64 ? slots : slots / 2);
   }
   const size_t dkv = p.dkv_splits > 1 ? (size_t)p.dkv_splits * 2 * keys * s.d * 4 : 0;
-  p.part = up256(dq > dkv ? dq : dkv);
+  p.dq_part = up256(dkv);
+  p.part = p.dq_part + up256(dq);
   return p;
 }
 
@@ -512,18 +514,23 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   unsigned int* err = error_word();
   if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");
   LaunchLog log{};
+  const bool with_q = p.tc && cross_tc_dkv_forms_dq(s.Nk, s.d);
   cudaError_t e = launch_cross_delta(a, dtype, cs, log);
   if (e == cudaSuccess && s.Nk > 0) {
     a.splits = p.dkv_splits;
     e = p.tc ? launch_cross_tc_dkv(a, err, cs, log) : launch_cross_simt_dkv(a, dtype, cs, log);
-    void* const outs[2] = {dK, dV};
-    if (e == cudaSuccess && a.splits > 1) e = launch_partial_sum(dtype, a.part, a.splits, outs, 2, kn, cs, log);
   }
-  if (e == cudaSuccess && !(p.tc && cross_tc_dkv_forms_dq(s.Nk, s.d))) {
-    a.splits = p.tc ? p.rounds.splits : p.dq_splits;
-    a.whole = p.rounds.whole;
-    e = p.tc ? launch_cross_tc_dq(a, err, cs, log) : launch_cross_simt_dq(a, dtype, cs, log);
-    if (e == cudaSuccess && p.dq_splits > 1) e = launch_partial_sum(dtype, a.part, p.dq_splits, &dQ, 1, qn, cs, log);
+  if (e == cudaSuccess && !with_q) {
+    CrossArgs q = a;
+    q.splits = p.tc ? p.rounds.splits : p.dq_splits;
+    q.whole = p.rounds.whole;
+    q.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.dq_part);
+    e = p.tc ? launch_cross_tc_dq(q, err, cs, log) : launch_cross_simt_dq(q, dtype, cs, log);
+    if (e == cudaSuccess && p.dq_splits > 1) e = launch_partial_sum(dtype, q.part, p.dq_splits, &dQ, 1, qn, cs, log);
+  }
+  if (e == cudaSuccess && s.Nk > 0 && p.dkv_splits > 1) {
+    void* const both[2] = {dK, dV};
+    e = launch_partial_sum(dtype, a.part, p.dkv_splits, both, 2, kn, cs, log);
   }
   return api_finish(e, "cross attention backward launch", log);
 }
