@@ -216,9 +216,9 @@ struct Rounds {
   int whole = 0, splits = 1;
   long long parts = 0;  // partial results
 };
-Rounds rounds_of(long long items, long long units) {
+Rounds rounds_of(long long items, long long units, long long sms) {
   Rounds r;
-  const long long sms = num_sms(), rest = items % sms;
+  const long long rest = items % sms;
   long long n = rest > 0 ? sms / rest : 1;
   if (n > units / 4) n = units / 4;
   if (n > 64) n = 64;
@@ -255,7 +255,7 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   if (!backward) {
     p.few = p.tc ? shared * s.Nq <= few_rows(s.d) : dt == AVQ_F32 && shared * s.Nq <= kFewRowsF32;
     if (p.tc && !p.few) {  // pairs of 128-row tiles
-      p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 255) / 256), key_tiles);
+      p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 255) / 256), key_tiles, num_sms());
       p.part = up256((size_t)p.rounds.parts * 256 * s.d * 4);
       p.part_lse = up256((size_t)p.rounds.parts * 256 * 4);
       return p;
@@ -279,9 +279,16 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   // dQ may be formed while dK and dV are: each in a place of its own
   size_t dq;
   if (p.tc) {
-    p.rounds = rounds_of((long long)s.B * s.Hq * ((s.Nq + 127) / 128), key_tiles);
+    const long long kb = (long long)s.Bk * s.Hk * key_tiles, qb = (long long)s.B * s.Hq * ((s.Nq + 127) / 128);
+    const long long sms = num_sms();
+    // Where the items of both kernels fit the SMs, neither is cut into more than leave
+    // the other its place, and they run side by side: 300 rows and keys, 24 heads of
+    // 128: 20.8 us, 32.5 with both over all SMs, one after the other; 1024 rows and
+    // keys, 8 heads of 64: 22.5 and 33.6.
+    const bool beside = kb + qb <= sms && !cross_tc_dkv_forms_dq(s.Nk, s.d);
+    p.dkv_splits = split_count(kb, shared * ((s.Nq + 127) / 128), beside ? sms * 4 / 7 : sms);
+    p.rounds = rounds_of(qb, key_tiles, beside ? sms - kb * p.dkv_splits : sms);
     dq = (size_t)p.rounds.parts * 128 * s.d * 4;
-    p.dkv_splits = split_count((long long)s.Bk * s.Hk * key_tiles, shared * ((s.Nq + 127) / 128), num_sms());
   } else {
     p.dq_splits = even_split(row_items, tiles64(s.Nk), slots);
     dq = p.dq_splits > 1 ? (size_t)p.dq_splits * rows * s.d * 4 : 0;
