@@ -568,17 +568,19 @@ def _qk_dims(Q, K, norm, eps, freqs, positions, layout, mscale, axes):
     B, Hq, N, d = Q.shape
     Hk = 0
     if K is not None:
-        if not isinstance(K, torch.Tensor) or K.dim() != 4 or (K.shape[0], K.shape[2], K.shape[3]) != (B, N, d):
+        shape = K.shape if isinstance(K, torch.Tensor) else ()
+        if len(shape) != 4 or shape[0] != B or shape[2] != N or shape[3] != d:
             raise ValueError("K must be [B, Hk, N, d] like Q")
-        Hk = K.shape[1]
+        Hk = shape[1]
     rot, pos_batch = 0, 0
     if freqs is not None:
-        rot = 2 * freqs.numel()
-        _expect(freqs, "freqs", (freqs.numel(),), torch.float64, Q.device)
+        pairs = freqs.numel()
+        rot, dev = 2 * pairs, Q.device
+        _expect(freqs, "freqs", (pairs,), torch.float64, dev)
         if positions is not None:
             tail = (2,) if axes == 2 else ()
             pos_batch = int(positions.dim() == 2 + len(tail))
-            _expect(positions, "positions", ((B, N) if pos_batch else (N,)) + tail, torch.int32, Q.device)
+            _expect(positions, "positions", ((B, N) if pos_batch else (N,)) + tail, torch.int32, dev)
     elif positions is not None:
         raise ValueError("positions need freqs")
     dims = avq_qk_dims(B, N, Hq, Hk, d, rot, int(axes), pos_batch, _choice(_LAYOUTS, layout, "layout"), norm,
@@ -587,14 +589,16 @@ def _qk_dims(Q, K, norm, eps, freqs, positions, layout, mscale, axes):
 
 
 def _qk_outputs(Q, K, Yq, Yk):
-    _expect(Yq, "the queries' output", Q.shape, Q.dtype, Q.device)
     if Yq is None:
         Yq = _dense_like(Q)
+    else:
+        _expect(Yq, "the queries' output", Q.shape, Q.dtype, Q.device)
     if K is None:
         return Yq, None
-    _expect(Yk, "the keys' output", K.shape, Q.dtype, Q.device)
     if Yk is None:
         Yk = _dense_like(K)
+    else:
+        _expect(Yk, "the keys' output", K.shape, Q.dtype, Q.device)
     return Yq, Yk
 
 
@@ -643,8 +647,10 @@ def avq_qk_norm(Q, K=None, q_weight=None, k_weight=None, q_bias=None, k_bias=Non
     dt, dev = _dtype_code(Q), Q.device
     qp, qs = _view(Q, "Q")
     kp, ks = _NO_VIEW if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
+    shape = (dims.d,)
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (q_bias, "q_bias"), (k_bias, "k_bias")):
-        _expect(t, n, (dims.d,), Q.dtype, dev)
+        if t is not None:
+            _expect(t, n, shape, Q.dtype, dev)
     with _Launch(dev, stream) as st:
         Yq, Yk = _qk_outputs(Q, K, Yq, Yk)
         _check(lib().avq_qk_norm(ctypes.byref(dims), dt, qp, ctypes.byref(qs), kp, ctypes.byref(ks), _addr(q_weight),
@@ -755,7 +761,8 @@ def avq_cross_attention_backward(dO, Q, K, V, O, lse, kv_lens=None, key_mask=Non
         raise ValueError("lse is needed: call the forward pass with lse=True")
     _expect(lse, "lse", Q.shape[:3], torch.float32, dev)
     for t, name, like in ((dQ, "dQ", Q), (dK, "dK", K), (dV, "dV", K)):
-        _expect(t, name, like.shape, Q.dtype, dev)
+        if t is not None:
+            _expect(t, name, like.shape, Q.dtype, dev)
     with _Launch(dev, stream) as st:
         dQ, dK, dV = (_dense_like(like) if t is None else t
                       for t, like in ((dQ, Q), (dK, K), (dV, K)))

@@ -426,3 +426,47 @@ def test_cross_f32_few_rows_captured():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(O, -want)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("dims", [
+    (2, 2, 8, 8, 300, 300, 128),    # both gradient kernels side by side
+    (1, 1, 4, 2, 200, 1500, 64),    # dQ split
+    (2, 1, 4, 2, 1500, 200, 128),   # dK and dV split
+    (4, 4, 8, 8, 500, 700, 64),     # neither fits beside the other
+    (2, 2, 4, 4, 600, 77, 64),      # one key tile
+])
+def test_cross_backward_calls_in_a_row_share_a_workspace(dims, dtype):
+    sets = []
+    for seed in (1, 2):
+        Q, K, V, dO, _ = inputs(*dims, DT[dtype], seed)
+        O, lse = avq.avq_cross_attention(Q, K, V, lse=True)
+        sets.append((dO, Q, K, V, O, lse))
+    want = []
+    for s in sets:
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in avq.avq_cross_attention_backward(*s)])
+    d = avq.avq_cross_dims(*dims, dims[-1] ** -0.5)
+    size = avq.avq_cross_workspace_size(d, avq.AVQ_BF16 if dtype == "bf16" else avq.AVQ_F32, True)
+    ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+
+    def round_():
+        return [avq.avq_cross_attention_backward(*sets[i], ws=ws) for i in (0, 1, 0, 1, 1, 0)]
+
+    torch.cuda.synchronize()
+    for k in range(3):
+        ws.fill_(255)
+        got = round_()
+        for i, g in zip((0, 1, 0, 1, 1, 0), got):
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        got = round_()
+    for k in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for i, g in zip((0, 1, 0, 1, 1, 0), got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+    avq.avq_check_device()
