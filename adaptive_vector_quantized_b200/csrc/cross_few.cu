@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
     *sAbort = 0;
   }
   __syncthreads();
+  grid_dependency_wait();  // the inputs, and whoever still reads the outputs
+  allow_dependents();
   const Guard guard{err, sAbort};
 
   if (warp == kWarps) {
@@ -319,8 +321,7 @@ cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int items = a.Bk * a.Hk * chunks * a.splits;
   const int grid = items < 2 * num_sms() ? items : 2 * num_sms();
-  cross_few_kernel<D, ROWS><<<grid, kThreads, smem, st>>>(k, v, a, err, items, chunks);
-  return cudaGetLastError();
+  return launch_after(cross_few_kernel<D, ROWS>, dim3(grid), dim3(kThreads), smem, st, k, v, a, err, items, chunks);
 }
 
 }  // namespace

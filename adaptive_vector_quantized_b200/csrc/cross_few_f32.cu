@@ -39,6 +39,8 @@ __global__ void __launch_bounds__(kThreads, 3) cross_few_f32_kernel(const CrossA
   constexpr int P = R::kPieces;
   extern __shared__ __align__(16) float4 ring[];
   __shared__ float sM[kGroups][kRows], sZ[kGroups][kRows];
+  grid_dependency_wait();
+  allow_dependents();
   const int lane = threadIdx.x & 31, group = threadIdx.x / 8, t = threadIdx.x % 8;
   const int chunk = blockIdx.x % chunks, kvh = blockIdx.x / chunks, split = blockIdx.y;
   const int kb = kvh / a.Hk, kh = kvh % a.Hk;
@@ -198,8 +200,7 @@ cudaError_t run(const CrossArgs& a, cudaStream_t st) {
   const cudaError_t e = allow_smem<cross_few_f32_kernel<D>>(Ring<D>::kBytes);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.Bk * a.Hk * chunks, a.splits);
-  cross_few_f32_kernel<D><<<grid, kThreads, Ring<D>::kBytes, st>>>(a, chunks);
-  return cudaGetLastError();
+  return launch_after(cross_few_f32_kernel<D>, grid, dim3(kThreads), Ring<D>::kBytes, st, a, chunks);
 }
 
 }  // namespace

@@ -138,6 +138,8 @@ __global__ void __launch_bounds__(kThreads) partial_sum_kernel(const float* part
 // delta[row] = sum_d dO O, one row per d / 8 lanes: dO and O read once.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cross_delta_kernel(const CrossArgs a) {
+  grid_dependency_wait();
+  allow_dependents();
   constexpr int L = D / 8;
   const long long rows = (long long)a.B * a.Hq * a.Nq;
   const long long row = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
@@ -215,14 +217,9 @@ cudaError_t launch_cross_delta(const CrossArgs& a, avq_dtype dt, cudaStream_t st
   const int per = kThreads / (a.d / 8);
   const unsigned grid = (unsigned)((rows + per - 1) / per);
   log.add("cross_delta");
-  if (dt == AVQ_F32) {
-    if (a.d == 64) cross_delta_kernel<float, 64><<<grid, kThreads, 0, st>>>(a);
-    else cross_delta_kernel<float, 128><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    if (a.d == 64) cross_delta_kernel<bf16, 64><<<grid, kThreads, 0, st>>>(a);
-    else cross_delta_kernel<bf16, 128><<<grid, kThreads, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  const auto kernel = dt == AVQ_F32 ? (a.d == 64 ? cross_delta_kernel<float, 64> : cross_delta_kernel<float, 128>)
+                                    : (a.d == 64 ? cross_delta_kernel<bf16, 64> : cross_delta_kernel<bf16, 128>);
+  return launch_after(kernel, dim3(grid), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace avq

@@ -145,6 +145,7 @@ __device__ __forceinline__ void clear(float2 (&acc)[kM][C]) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2) cross_simt_kernel(const CrossArgs a) {
+  grid_dependency_wait();
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
   float* sKV = sQ + kT * D;  // K, then V
@@ -261,7 +262,8 @@ __device__ __forceinline__ void load_rows(const CrossArgs& a, float* sL, float* 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kernel(const CrossArgs a) {
-  allow_dependents();  // dQ's blocks may take the places that these leave
+  grid_dependency_wait();  // delta
+  allow_dependents();      // dQ's blocks may take the places that these leave
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
   float* sV = sK + kT * D;
@@ -410,8 +412,7 @@ cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
   cudaError_t e = allow_smem<cross_simt_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
-  cross_simt_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(cross_simt_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
 }
 template <typename T, int D>
 cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
@@ -419,8 +420,7 @@ cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
   cudaError_t e = allow_smem<cross_simt_dkv_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT)), a.splits);
-  cross_simt_dkv_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(cross_simt_dkv_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
 }
 template <typename T, int D>
 cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
@@ -428,7 +428,7 @@ cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
   cudaError_t e = allow_smem<cross_simt_dq_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
-  // dK and dV's kernel started after delta was complete and writes nothing that is read here
+  // dK and dV's kernel waited for delta and writes nothing that is read here
   return launch_after(cross_simt_dq_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
 }
 

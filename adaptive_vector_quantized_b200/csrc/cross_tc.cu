@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  grid_dependency_wait();  // the inputs, and whoever still reads the outputs
   const Guard guard{err, sAbort};
   const uint32_t tmem = *sTmem;
   // columns: S of each tile, the halves of a key tile apart | O0 | O1
@@ -539,8 +540,7 @@ cudaError_t run(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLo
   const int items = a.B * a.Hq * pairs;
   const int launch = a.whole + (items - a.whole) * a.splits;
   const int grid = launch < num_sms() ? launch : num_sms();
-  cross_tc_kernel<D><<<grid, kThreads, smem, st>>>(m, a, err, launch, pairs);
-  e = cudaGetLastError();
+  e = launch_after(cross_tc_kernel<D>, dim3(grid), dim3(kThreads), smem, st, m, a, err, launch, pairs);
   if (e == cudaSuccess && a.whole < items) e = launch_cross_join_items(a, items, pairs, 2 * kRowTile, true, st, log);
   return e;
 }

@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_kernel(const Params p) {
       if (k * slots < left) places.request((i & 1) * U + k, x, apart);
     tc::cp_async_commit();
   };
+  grid_dependency_wait();
   request(0);  // under way while the angles are made
   request(1);
   if constexpr (kNorm != AVQ_NORM_NONE) fill_weights<T, D>(p, sw, sb);
@@ -319,6 +320,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Par
   constexpr int L = D / 8, G = kThreads / L, U = kBatch<T> / 2;
   __shared__ __align__(16) typename Raw<T>::Four ring[kStages * U * 4 * kThreads];
   float* sums = reinterpret_cast<float*>(ring);  // [G][D], at the end
+  grid_dependency_wait();
+  allow_dependents();
   const int which = blockIdx.y;
   const int H = p.H[which];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -537,27 +540,23 @@ Params params_of(const avq_qk_dims& s, const Strides* xs, const int32_t* pos, co
 }
 
 template <typename T, int D, int kNorm>
-void launch_fwd(const Params& p, bool half, int tiles, cudaStream_t st) {
-  if (half)
-    qk_norm_kernel<T, D, kNorm, true><<<tiles, kThreads, 0, st>>>(p);
-  else
-    qk_norm_kernel<T, D, kNorm, false><<<tiles, kThreads, 0, st>>>(p);
+cudaError_t launch_fwd(const Params& p, bool half, int tiles, cudaStream_t st) {
+  return launch_after(half ? qk_norm_kernel<T, D, kNorm, true> : qk_norm_kernel<T, D, kNorm, false>, dim3(tiles),
+                      dim3(kThreads), 0, st, p);
 }
 template <typename T, int D>
-void launch_fwd_norm(const Params& p, int norm, bool half, int tiles, cudaStream_t st) {
+cudaError_t launch_fwd_norm(const Params& p, int norm, bool half, int tiles, cudaStream_t st) {
   if (norm == AVQ_NORM_NONE) return launch_fwd<T, D, AVQ_NORM_NONE>(p, half, tiles, st);
   if (norm == AVQ_NORM_RMS) return launch_fwd<T, D, AVQ_NORM_RMS>(p, half, tiles, st);
   return launch_fwd<T, D, AVQ_NORM_LAYER>(p, half, tiles, st);
 }
 template <typename T, int D, int kNorm>
-void launch_bwd(const Params& p, bool half, int tiles, dim3 grid, cudaStream_t st) {
-  if (half)
-    qk_norm_backward_kernel<T, D, kNorm, true><<<grid, kThreads, 0, st>>>(p, tiles);
-  else
-    qk_norm_backward_kernel<T, D, kNorm, false><<<grid, kThreads, 0, st>>>(p, tiles);
+cudaError_t launch_bwd(const Params& p, bool half, int tiles, dim3 grid, cudaStream_t st) {
+  return launch_after(half ? qk_norm_backward_kernel<T, D, kNorm, true> : qk_norm_backward_kernel<T, D, kNorm, false>,
+                      grid, dim3(kThreads), 0, st, p, tiles);
 }
 template <typename T, int D>
-void launch_bwd_norm(const Params& p, int norm, bool half, int tiles, dim3 grid, cudaStream_t st) {
+cudaError_t launch_bwd_norm(const Params& p, int norm, bool half, int tiles, dim3 grid, cudaStream_t st) {
   if (norm == AVQ_NORM_RMS) return launch_bwd<T, D, AVQ_NORM_RMS>(p, half, tiles, grid, st);
   return launch_bwd<T, D, AVQ_NORM_LAYER>(p, half, tiles, grid, st);
 }
@@ -580,15 +579,16 @@ cudaError_t launch_qk_norm(const avq_qk_dims& s, avq_dtype dt, const void* const
   if (inverse) p.sign = -1.f;
   const int tiles = (p.tokens + p.tb - 1) / p.tb;
   const bool half = s.layout == AVQ_ROTARY_HALF;
+  cudaError_t e;
   if (dt == AVQ_F32) {
-    if (s.d == 64) launch_fwd_norm<float, 64>(p, s.norm, half, tiles, st);
-    else launch_fwd_norm<float, 128>(p, s.norm, half, tiles, st);
+    e = s.d == 64 ? launch_fwd_norm<float, 64>(p, s.norm, half, tiles, st)
+                  : launch_fwd_norm<float, 128>(p, s.norm, half, tiles, st);
   } else {
-    if (s.d == 64) launch_fwd_norm<bf16, 64>(p, s.norm, half, tiles, st);
-    else launch_fwd_norm<bf16, 128>(p, s.norm, half, tiles, st);
+    e = s.d == 64 ? launch_fwd_norm<bf16, 64>(p, s.norm, half, tiles, st)
+                  : launch_fwd_norm<bf16, 128>(p, s.norm, half, tiles, st);
   }
   log.add(s.norm == AVQ_NORM_NONE ? "rotary" : "qk_norm");
-  return cudaGetLastError();
+  return e;
 }
 
 size_t qk_norm_backward_workspace(const avq_qk_dims& s) {
@@ -608,15 +608,15 @@ cudaError_t launch_qk_norm_backward(const avq_qk_dims& s, avq_dtype dt, const vo
   const bool half = s.layout == AVQ_ROTARY_HALF;
   const int blocks = backward_blocks(s);
   const dim3 grid(blocks, s.Hk > 0 ? 2 : 1);
+  cudaError_t e;
   if (dt == AVQ_F32) {
-    if (s.d == 64) launch_bwd_norm<float, 64>(p, s.norm, half, tiles, grid, st);
-    else launch_bwd_norm<float, 128>(p, s.norm, half, tiles, grid, st);
+    e = s.d == 64 ? launch_bwd_norm<float, 64>(p, s.norm, half, tiles, grid, st)
+                  : launch_bwd_norm<float, 128>(p, s.norm, half, tiles, grid, st);
   } else {
-    if (s.d == 64) launch_bwd_norm<bf16, 64>(p, s.norm, half, tiles, grid, st);
-    else launch_bwd_norm<bf16, 128>(p, s.norm, half, tiles, grid, st);
+    e = s.d == 64 ? launch_bwd_norm<bf16, 64>(p, s.norm, half, tiles, grid, st)
+                  : launch_bwd_norm<bf16, 128>(p, s.norm, half, tiles, grid, st);
   }
   log.add("qk_norm_backward");
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   bool any = false;
   for (int i = 0; i < 2; ++i) any = any || dw[i] != nullptr || db[i] != nullptr;
