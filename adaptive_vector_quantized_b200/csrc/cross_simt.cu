@@ -17,12 +17,14 @@
 // product.
 //
 // Bound by what shared memory hands to registers (32 values a clock and SM, each
-// used by 4 of 128 products a clock: half the FMA pipe's rate) and by the loads,
-// which the other block of the SM covers: K and V (in dQ: V and K) take the same
-// place one after the other, so two blocks fit.  24 heads of 1000 rows and keys of
-// 128: 463 us (26 TFLOP/s; 549 with a place for each, one block an SM), gradients
-// 1.51 ms (1.63).  8 x 4 scores a thread, with half the threads: 511 us and 1.77 ms,
-// as too few warps are left to cover anything.
+// used by 4 of 128 products a clock: half the FMA pipe's rate).  The loads of 32-bit
+// inputs run beside the products: V's beside Q K^T, the next K's beside P V, for dK
+// and dV the next step's rows beside this one's (in dQ V and K take one place, one
+// after the other, so that another block of the SM covers them).  24 heads of 1000
+// rows and keys of 128: 411 us (30 TFLOP/s; 463 with K and V in one place, 549 with
+// loads that nothing covers), gradients 1.35 ms (1.39 without the next rows).  8 x 4
+// scores a thread, with half the threads: 511 us where 4 x 4 took 463, as too few
+// warps are left to cover anything.
 #include "cross.cuh"
 #include "fastmath.cuh"
 
@@ -58,6 +60,26 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_
     if (want(r)) loadE<4>(src + (int64_t)(first + r) * row_stride + 4 * c, v);
     *reinterpret_cast<float4*>(dst + place<D>(r, c)) = make_float4(v[0], v[1], v[2], v[3]);
   }
+}
+
+// load_tile under way: complete after cp_async_wait and a barrier (bf16 has to be
+// converted, so its loads are complete at the barrier).
+template <typename T, int D, typename F>
+__device__ __forceinline__ void fetch_tile(float* dst, const T* src, int64_t row_stride, int first, F&& want) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+    for (int e = threadIdx.x; e < kT * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), c = e % (D / 4);
+      float* to = dst + place<D>(r, c);
+      if (want(r))
+        tc::cp_async16(to, src + (int64_t)(first + r) * row_stride + 4 * c);
+      else
+        *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  } else {
+    load_tile<T, D>(dst, src, row_stride, first, want);
+  }
+  tc::cp_async_commit();
 }
 
 // acc[i][j] = sum_k A[ty + 16 i][k] B[tx + 16 j][k]
@@ -148,9 +170,10 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_kernel(const CrossArgs
   grid_dependency_wait();
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
-  float* sKV = sQ + kT * D;  // K, then V
-  float* sP = sKV + kT * D;
-  __shared__ unsigned char seen[kT];
+  float* sK = sQ + kT * D;
+  float* sV = sK + kT * D;
+  float* sP = sV + kT * D;
+  __shared__ unsigned char seen[2][kT];
   const int tiles = (a.Nq + kT - 1) / kT;
   const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
   const int b = bh / a.Hq, h = bh % a.Hq;
@@ -163,7 +186,13 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_kernel(const CrossArgs
   const T* Q = static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h;
   const T* K = static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h;
   const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
-  load_tile<T, D>(sQ, Q, a.qs.n, row0, [&](int r) { return row0 + r < a.Nq; });
+  fetch_tile<T, D>(sQ, Q, a.qs.n, row0, [&](int r) { return row0 + r < a.Nq; });
+  auto look = [&](int t) {
+    if (threadIdx.x < kT && t < t1) seen[t & 1][threadIdx.x] = key_seen(a, kb, t * kT + threadIdx.x, count);
+  };
+  look(t0);
+  __syncthreads();
+  if (t0 < t1) fetch_tile<T, D>(sK, K, a.ks.n, t0 * kT, [&](int r) { return seen[t0 & 1][r] != 0; });
   const float c2 = a.scale * kLog2e;
   float m[kM], z[kM];
   float2 o[kM][D / 32];
@@ -171,22 +200,19 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_kernel(const CrossArgs
 #pragma unroll
   for (int i = 0; i < kM; ++i) m[i] = -INFINITY, z[i] = 0.f;
   for (int t = t0; t < t1; ++t) {
-    const int k0 = t * kT;
-    __syncthreads();  // the tiles below are still read by the last trip
-    if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
-    __syncthreads();
-    load_tile<T, D>(sKV, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
-    __syncthreads();
+    const unsigned char* on = seen[t & 1];
+    tc::cp_async_wait<0>();
+    __syncthreads();  // K is here; the last trip has read V and P
+    fetch_tile<T, D>(sV, V, a.vs.n, t * kT, [&](int r) { return on[r] != 0; });
+    look(t + 1);
     float s[kM][4];
-    rows_rows<D>(sQ, sKV, ty, tx, s);
-    __syncthreads();
-    load_tile<T, D>(sKV, V, a.vs.n, k0, [&](int r) { return seen[r] != 0; });
+    rows_rows<D>(sQ, sK, ty, tx, s);
 #pragma unroll
     for (int i = 0; i < kM; ++i) {
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (!seen[tx + 16 * j]) s[i][j] = -INFINITY;
+        if (!on[tx + 16 * j]) s[i][j] = -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
@@ -205,9 +231,13 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_kernel(const CrossArgs
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) o[i][c] = fm::mul2(o[i][c], fm::f2(keep, keep));
     }
-    __syncthreads();
-    rows_cols<D>(sP, sKV, ty, tx, o);
+    tc::cp_async_wait<0>();
+    __syncthreads();  // V and P are here; K has been read
+    if (t + 1 < t1)
+      fetch_tile<T, D>(sK, K, a.ks.n, (t + 1) * kT, [&](int r) { return seen[(t + 1) & 1][r] != 0; });
+    rows_cols<D>(sP, sV, ty, tx, o);
   }
+  tc::cp_async_wait<0>();  // without steps Q is still under way
 #pragma unroll
   for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -260,6 +290,11 @@ __device__ __forceinline__ void load_rows(const CrossArgs& a, float* sL, float* 
   }
 }
 
+// At d = 128 one block fits an SM either way, with room for the next step's rows; at
+// 64 two blocks do without it.
+template <int D>
+constexpr int kRowBufs = D == 64 ? 1 : 2;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kernel(const CrossArgs a) {
   grid_dependency_wait();  // delta
@@ -267,11 +302,11 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;
   float* sV = sK + kT * D;
-  float* sQ = sV + kT * D;
-  float* sG = sQ + kT * D;
-  float* sP = sG + kT * D;
+  constexpr int N = kRowBufs<D>;
+  float* rows = sV + kT * D;  // Q and dO, of this step and with two places of the next
+  float* sP = rows + N * 2 * kT * D;
   float* sD = sP + kT * kT;
-  __shared__ float sL[kT], sDelta[kT];
+  __shared__ float sL[N][kT], sDelta[N][kT];
   __shared__ unsigned char seen[kT];
   const int tiles = (a.Nk + kT - 1) / kT;
   const int kt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
@@ -282,9 +317,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
   const int count = key_count(a, kb);
   if (threadIdx.x < kT) seen[threadIdx.x] = key_seen(a, kb, k0 + threadIdx.x, count);
   __syncthreads();
-  load_tile<T, D>(sK, static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h, a.ks.n, k0,
+  fetch_tile<T, D>(sK, static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h, a.ks.n, k0,
                   [&](int r) { return seen[r] != 0; });
-  load_tile<T, D>(sV, static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h, a.vs.n, k0,
+  fetch_tile<T, D>(sV, static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h, a.vs.n, k0,
                   [&](int r) { return seen[r] != 0; });
   const float c2 = a.scale * kLog2e;
   float2 dk[kM][D / 32], dv[kM][D / 32];
@@ -293,20 +328,31 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
   const int rtiles = (a.Nq + kT - 1) / kT;
   const int all = R * G * rtiles;
   const int i0 = part_begin(all, split, a.splits), i1 = k0 < count ? part_begin(all, split + 1, a.splits) : i0;
-  for (int it = i0; it < i1; ++it) {
-    const int row0 = it % rtiles * kT, rg = it / rtiles;
+  auto fetch = [&](int it) {
+    if (it >= i1) return;
+    const int row0 = it % rtiles * kT, rg = it / rtiles, place = (it - i0) % N;
     const int b = kb * R + rg / G, h = kh * G + rg % G;
-    __syncthreads();
-    load_tile<T, D>(sQ, static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h, a.qs.n, row0,
-                    [&](int r) { return row0 + r < a.Nq; });
-    load_tile<T, D>(sG, static_cast<const T*>(a.G) + b * a.gs.b + h * a.gs.h, a.gs.n, row0,
-                    [&](int r) { return row0 + r < a.Nq; });
-    load_rows(a, sL, sDelta, ((size_t)b * a.Hq + h) * a.Nq, row0);
-    __syncthreads();
+    float* to = rows + place * 2 * kT * D;
+    auto in = [&](int r) { return row0 + r < a.Nq; };
+    fetch_tile<T, D>(to, static_cast<const T*>(a.Q) + b * a.qs.b + h * a.qs.h, a.qs.n, row0, in);
+    fetch_tile<T, D>(to + kT * D, static_cast<const T*>(a.G) + b * a.gs.b + h * a.gs.h, a.gs.n, row0, in);
+    load_rows(a, sL[place], sDelta[place], ((size_t)b * a.Hq + h) * a.Nq, row0);
+  };
+  if (N > 1) fetch(i0);
+  for (int it = i0; it < i1; ++it) {
+    const int place = (it - i0) % N;
+    const float *sQ = rows + place * 2 * kT * D, *sG = sQ + kT * D;
+    if (N == 1) {
+      __syncthreads();  // the last trip has read the rows
+      fetch(it);
+    }
+    tc::cp_async_wait<0>();
+    __syncthreads();  // this step's rows are here; the last trip has read its own and P and dS
+    if (N > 1) fetch(it + 1);
     float p[kM][4], ds[kM][4];
     rows_rows<D>(sQ, sK, ty, tx, p);
     rows_rows<D>(sG, sV, ty, tx, ds);
-    scores_back(sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
+    scores_back(sL[place], sDelta[place], seen, ty, tx, c2, a.scale, p, ds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -318,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
     cols_cols<D>(sP, sG, ty, tx, dv);
     cols_cols<D>(sD, sQ, ty, tx, dk);
   }
+  tc::cp_async_wait<0>();  // without steps K and V are still under way
   const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
@@ -408,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
 
 template <typename T, int D>
 cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(2 * kT * D + kT * kT) * sizeof(float);
+  const size_t smem = (size_t)(3 * kT * D + kT * kT) * sizeof(float);
   cudaError_t e = allow_smem<cross_simt_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
@@ -416,7 +463,7 @@ cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
 }
 template <typename T, int D>
 cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(4 * kT * D + 2 * kT * kT) * sizeof(float);
+  const size_t smem = (size_t)((2 + 2 * kRowBufs<D>) * kT * D + 2 * kT * kT) * sizeof(float);
   cudaError_t e = allow_smem<cross_simt_dkv_kernel<T, D>>((int)smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT)), a.splits);

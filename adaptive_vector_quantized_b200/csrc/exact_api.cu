@@ -185,7 +185,7 @@ long long tiles64(long long n) { return (n + 63) / 64; }
 // `slots` resident blocks: as many as make the rounds shortest, where a part costs
 // about half a tile more (its own tile's load, its result's way to memory and back).
 // 12 heads of 1001 rows over 333 keys of 64 (192 items of up to 6 tiles): 45 us, 55 with
-// as many parts as the slots hold at once.
+// as many parts as the slots hold at once (41 us now).
 int even_split(long long items, long long units, long long slots) {
   int best = 1;
   double least = 0;
@@ -203,9 +203,9 @@ int even_split(long long items, long long units, long long slots) {
 constexpr long long few_rows(int d) { return d == 64 ? 32 : 16; }
 
 // The same for 32-bit inputs, four rows at a time against 64-row tiles: 8 sequences of
-// 4096 keys, 8 heads, 8 rows take 46 against 182 us at d = 64 and 63 against 346 at
-// d = 128, 32 rows 182 against 182 and 259 against 348, 48 rows 218 against 183 at d = 64.
-constexpr long long kFewRowsF32 = 32;
+// 4096 keys, 8 heads, 8 rows take 46 against 144 us at d = 64 and 63 against 270 at
+// d = 128, 24 rows 115 against 145 and 161 against 270, 32 rows 181 and 258.
+constexpr long long kFewRowsF32 = 24;
 
 // How the items of a kernel with one block per SM, each a walk over `units` key
 // tiles, fill its rounds: the items of full rounds stay whole, those of the last

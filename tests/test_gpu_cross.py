@@ -406,7 +406,7 @@ def test_layer_as_it_is_used():
 def test_cross_f32_few_rows(dims, lens, mask, d):
     B, Bk, Hq, Hk, Nq, Nk = dims
     kernels = run_case(B, Bk, Hq, Hk, Nq, Nk, d, "f32", lens, mask, packed=B % 2 == 0)
-    assert ("cross_few_f32" in kernels) == (B // Bk * (Hq // Hk) * Nq <= 32)
+    assert ("cross_few_f32" in kernels) == (B // Bk * (Hq // Hk) * Nq <= 24)
 
 
 def test_cross_f32_few_rows_captured():
