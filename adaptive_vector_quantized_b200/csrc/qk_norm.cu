@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_kernel(const Params p) {
 // Gradients.  blockIdx.y: queries or keys; each block walks tiles and keeps
 // its share of the weight gradients in registers, summed over its groups at
 // the end in a fixed order.
-template <typename T, int D, int kNorm, bool kHalf>
+template <typename T, int D, int kNorm, bool kHalf, bool kBias>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Params p, int tiles) {
   constexpr int L = D / 8, G = kThreads / L, U = kBatch<T> / 2;
   __shared__ __align__(16) typename Raw<T>::Four ring[kStages * U * 4 * kThreads];
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Par
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         dw[e] = fm::fma2(z[k][e], u[k][e], dw[e]);
-        db[e] = fm::add2(db[e], z[k][e]);
+        if constexpr (kBias) db[e] = fm::add2(db[e], z[k][e]);
         z[k][e] = fm::mul2(z[k][e], w[e]);
         gu = fm::fma2(z[k][e], u[k][e], gu);
         if constexpr (kNorm == AVQ_NORM_LAYER) gm = fm::add2(gm, z[k][e]);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_backward_kernel(const Par
     turn_of(1);
   }
   tc::cp_async_wait<0>();
-  for (int kind = 0; kind < 2; ++kind) {
+  for (int kind = 0; kind < (kBias ? 2 : 1); ++kind) {
     __syncthreads();
     store4(sums + group * D + ia, kind == 0 ? dw : db);
     store4(sums + group * D + ib, kind == 0 ? dw + 2 : db + 2);
@@ -550,15 +550,20 @@ cudaError_t launch_fwd_norm(const Params& p, int norm, bool half, int tiles, cud
   if (norm == AVQ_NORM_RMS) return launch_fwd<T, D, AVQ_NORM_RMS>(p, half, tiles, st);
   return launch_fwd<T, D, AVQ_NORM_LAYER>(p, half, tiles, st);
 }
-template <typename T, int D, int kNorm>
+template <typename T, int D, int kNorm, bool kBias>
 cudaError_t launch_bwd(const Params& p, bool half, int tiles, dim3 grid, cudaStream_t st) {
-  return launch_after(half ? qk_norm_backward_kernel<T, D, kNorm, true> : qk_norm_backward_kernel<T, D, kNorm, false>,
+  return launch_after(half ? qk_norm_backward_kernel<T, D, kNorm, true, kBias>
+                           : qk_norm_backward_kernel<T, D, kNorm, false, kBias>,
                       grid, dim3(kThreads), 0, st, p, tiles);
 }
+// bias: whether a bias gradient is asked for
 template <typename T, int D>
-cudaError_t launch_bwd_norm(const Params& p, int norm, bool half, int tiles, dim3 grid, cudaStream_t st) {
-  if (norm == AVQ_NORM_RMS) return launch_bwd<T, D, AVQ_NORM_RMS>(p, half, tiles, grid, st);
-  return launch_bwd<T, D, AVQ_NORM_LAYER>(p, half, tiles, grid, st);
+cudaError_t launch_bwd_norm(const Params& p, int norm, bool bias, bool half, int tiles, dim3 grid, cudaStream_t st) {
+  if (norm == AVQ_NORM_RMS)
+    return bias ? launch_bwd<T, D, AVQ_NORM_RMS, true>(p, half, tiles, grid, st)
+                : launch_bwd<T, D, AVQ_NORM_RMS, false>(p, half, tiles, grid, st);
+  return bias ? launch_bwd<T, D, AVQ_NORM_LAYER, true>(p, half, tiles, grid, st)
+              : launch_bwd<T, D, AVQ_NORM_LAYER, false>(p, half, tiles, grid, st);
 }
 
 int backward_blocks(const avq_qk_dims& s) {
@@ -607,14 +612,15 @@ cudaError_t launch_qk_norm_backward(const avq_qk_dims& s, avq_dtype dt, const vo
   const int tiles = (p.tokens + p.tb - 1) / p.tb;
   const bool half = s.layout == AVQ_ROTARY_HALF;
   const int blocks = backward_blocks(s);
+  const bool bias = db[0] != nullptr || db[1] != nullptr;
   const dim3 grid(blocks, s.Hk > 0 ? 2 : 1);
   cudaError_t e;
   if (dt == AVQ_F32) {
-    e = s.d == 64 ? launch_bwd_norm<float, 64>(p, s.norm, half, tiles, grid, st)
-                  : launch_bwd_norm<float, 128>(p, s.norm, half, tiles, grid, st);
+    e = s.d == 64 ? launch_bwd_norm<float, 64>(p, s.norm, bias, half, tiles, grid, st)
+                  : launch_bwd_norm<float, 128>(p, s.norm, bias, half, tiles, grid, st);
   } else {
-    e = s.d == 64 ? launch_bwd_norm<bf16, 64>(p, s.norm, half, tiles, grid, st)
-                  : launch_bwd_norm<bf16, 128>(p, s.norm, half, tiles, grid, st);
+    e = s.d == 64 ? launch_bwd_norm<bf16, 64>(p, s.norm, bias, half, tiles, grid, st)
+                  : launch_bwd_norm<bf16, 128>(p, s.norm, bias, half, tiles, grid, st);
   }
   log.add("qk_norm_backward");
   if (e != cudaSuccess) return e;
