@@ -141,19 +141,19 @@ __device__ __forceinline__ bool places(int lane, int rot, int& a, int& b) {
   return turned;
 }
 
-// A lane's four rotations, as factors of two elements at a time: for the half
-// layout c = (c0, c1), s = (s0, s1) of neighbouring pairs, interleaved c = (c, c),
-// s = (-s, s) of one pair.
+// A lane's four rotations.  In the half layout pairs are neighbours in each of the
+// two groups: two at a time, c = (c0, c1).  Interleaved, an element's partner is its
+// neighbour: one at a time, since (c, c) and (-s, s) would take twice the registers
+// and the swap two moves.
 template <bool kHalf>
 struct Turn {
-  static constexpr int kN = kHalf ? 2 : 4;
-  float2 c[kN], s[kN];
+  float2 c[2], s[2];
   // of the angles with cosines x and sines y
   __device__ __forceinline__ void set(const float* x, const float* y) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      c[i] = kHalf ? fm::f2(x[2 * i], x[2 * i + 1]) : fm::f2(x[i], x[i]);
-      s[i] = kHalf ? fm::f2(y[2 * i], y[2 * i + 1]) : fm::f2(-y[i], y[i]);
+    for (int i = 0; i < 2; ++i) {
+      c[i] = fm::f2(x[2 * i], x[2 * i + 1]);
+      s[i] = fm::f2(y[2 * i], y[2 * i + 1]);
     }
   }
   // v: the lane's elements two by two, group a then group b
@@ -168,7 +168,11 @@ struct Turn {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fm::fma2(v[i], c[i], fm::mul2(fm::f2(v[i].y, v[i].x), s[i]));
+      for (int i = 0; i < 4; ++i) {
+        const float ci = i & 1 ? c[i >> 1].y : c[i >> 1].x, si = i & 1 ? s[i >> 1].y : s[i >> 1].x;
+        const float2 x = v[i];
+        v[i] = fm::f2(fmaf(x.x, ci, -(x.y * si)), fmaf(x.y, ci, x.x * si));
+      }
     }
   }
 };
