@@ -674,12 +674,13 @@ def avq_qk_norm_backward(dYq, dYk, Q, K=None, q_weight=None, k_weight=None, norm
     qp, qs = _view(Q, "Q")
     kp, ks = _NO_VIEW if K is None else _view(K, "K", dtype=Q.dtype, device=dev)
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _expect(t, n, (dims.d,), Q.dtype, dev)
-    wanted = (q_weight is not None, K is not None and k_weight is not None, bias, bias and K is not None)
+        if t is not None:
+            _expect(t, n, (dims.d,), Q.dtype, dev)
+    wanted = (q_weight is not None, K is not None and k_weight is not None, bool(bias), bool(bias) and K is not None)
     with _Launch(dev, stream) as st:
         dQ, dK = _qk_outputs(Q, K, dQ, dK)
-        sums = torch.empty((4, dims.d), dtype=torch.float32, device=dev).unbind(0)
-        dwq, dwk, dbq, dbk = (x if w else None for x, w in zip(sums, wanted))
+        sums = iter(torch.empty((sum(wanted), dims.d), dtype=torch.float32, device=dev).unbind(0) if any(wanted) else ())
+        dwq, dwk, dbq, dbk = (next(sums) if w else None for w in wanted)
         if ws is None:
             n = int(lib().avq_qk_norm_workspace_size(ctypes.byref(dims), dt))
             ws = torch.empty(n + 256, dtype=torch.uint8, device=dev)

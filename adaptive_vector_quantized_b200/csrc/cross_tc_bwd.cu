@@ -913,41 +913,47 @@ cudaError_t maps_of(const CrossArgs& a, Maps* m) {
   return e;
 }
 
-template <int D, bool kWithQ>
-cudaError_t run_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st) {
-  Maps m;
-  const Strides s = dense(a.Bk, a.Hk, a.Nk, D);
-  cudaError_t e = maps_of<D>(a, &m);
-  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dV, s, a.Bk, a.Hk, a.Nk, D, 32);
-  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, s, a.Bk, a.Hk, a.Nk, D, 32);
-  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out2, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
-  if (e != cudaSuccess) return e;
-  constexpr int smem = Smem<D>::kTotal;
-  e = allow_smem<cross_tc_dkv_kernel<D, kWithQ>>(smem);
-  if (e != cudaSuccess) return e;
-  const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
-  const int items = a.Bk * a.Hk * ktiles * a.splits;
-  const dim3 grid(items < num_sms() ? items : num_sms());
-  return launch_after(cross_tc_dkv_kernel<D, kWithQ>, grid, dim3(kThreads), smem, st, m, a, err, items, ktiles, rtiles);
-}
-
+// a, q: the arguments of the kernel of dK and dV, and of dQ's.  Each tensor map
+// takes the host most of a microsecond: the inputs' serve both kernels.
 template <int D>
-cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
+cudaError_t run(const CrossArgs& a, const CrossArgs& q, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   Maps m;
+  const bool with_q = cross_tc_dkv_forms_dq(a.Nk, D);
+  const Strides ks = dense(a.Bk, a.Hk, a.Nk, D), qs = dense(a.B, a.Hq, a.Nq, D);
+  CUtensorMap dq;
   cudaError_t e = maps_of<D>(a, &m);
-  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dQ, dense(a.B, a.Hq, a.Nq, D), a.B, a.Hq, a.Nq, D, 32);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dV, ks, a.Bk, a.Hk, a.Nk, D, 32);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, ks, a.Bk, a.Hk, a.Nk, D, 32);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&dq, a.dQ, qs, a.B, a.Hq, a.Nq, D, 32);
   if (e != cudaSuccess) return e;
-  m.out1 = m.out2 = m.out0;
+  m.out2 = dq;
   constexpr int smem = Smem<D>::kTotal;
-  e = allow_smem<cross_tc_dq_kernel<D>>(smem);
+  const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
+  const int key_items = a.Bk * a.Hk * ktiles * a.splits;
+  const dim3 key_grid(key_items < num_sms() ? key_items : num_sms());
+  log.add(with_q ? "cross_tc_dqkv" : "cross_tc_dkv");
+  if constexpr (D == 64) {
+    if (with_q) {
+      e = allow_smem<cross_tc_dkv_kernel<D, true>>(smem);
+      if (e != cudaSuccess) return e;
+      return launch_after(cross_tc_dkv_kernel<D, true>, key_grid, dim3(kThreads), smem, st, m, a, err, key_items,
+                          ktiles, rtiles);
+    }
+  }
+  e = allow_smem<cross_tc_dkv_kernel<D, false>>(smem);
+  if (e == cudaSuccess) e = allow_smem<cross_tc_dq_kernel<D>>(smem);
+  if (e == cudaSuccess)
+    e = launch_after(cross_tc_dkv_kernel<D, false>, key_grid, dim3(kThreads), smem, st, m, a, err, key_items, ktiles,
+                     rtiles);
   if (e != cudaSuccess) return e;
-  const int rtiles = (a.Nq + 127) / 128;
+  m.out0 = dq;
   const int items = a.B * a.Hq * rtiles;
-  const int launch = a.whole + (items - a.whole) * a.splits;
-  const int grid = launch < num_sms() ? launch : num_sms();
+  const int launch = q.whole + (items - q.whole) * q.splits;
+  const dim3 grid(launch < num_sms() ? launch : num_sms());
+  log.add("cross_tc_dq");
   // dK and dV's kernel waited for delta and writes nothing that is read here
-  e = launch_after(cross_tc_dq_kernel<D>, dim3(grid), dim3(kThreads), smem, st, m, a, err, launch, rtiles);
-  if (e == cudaSuccess && a.whole < items) e = launch_cross_join_items(a, items, rtiles, 128, false, st, log);
+  e = launch_after(cross_tc_dq_kernel<D>, grid, dim3(kThreads), smem, st, m, q, err, launch, rtiles);
+  if (e == cudaSuccess && q.whole < items) e = launch_cross_join_items(q, items, rtiles, 128, false, st, log);
   return e;
 }
 
@@ -955,14 +961,9 @@ cudaError_t run_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, Launc
 
 bool cross_tc_dkv_forms_dq(int Nk, int d) { return d == 64 && Nk <= 128; }
 
-cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
-  log.add(cross_tc_dkv_forms_dq(a.Nk, a.d) ? "cross_tc_dqkv" : "cross_tc_dkv");
-  if (cross_tc_dkv_forms_dq(a.Nk, a.d)) return run_dkv<64, true>(a, err, st);
-  return a.d == 64 ? run_dkv<64, false>(a, err, st) : run_dkv<128, false>(a, err, st);
-}
-cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log) {
-  log.add("cross_tc_dq");
-  return a.d == 64 ? run_dq<64>(a, err, st, log) : run_dq<128>(a, err, st, log);
+cudaError_t launch_cross_tc_backward(const CrossArgs& a, const CrossArgs& q, unsigned int* err, cudaStream_t st,
+                                     LaunchLog& log) {
+  return a.d == 64 ? run<64>(a, q, err, st, log) : run<128>(a, q, err, st, log);
 }
 
 }  // namespace avq

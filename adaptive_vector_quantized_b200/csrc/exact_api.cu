@@ -521,18 +521,17 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   unsigned int* err = error_word();
   if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");
   LaunchLog log{};
-  const bool with_q = p.tc && cross_tc_dkv_forms_dq(s.Nk, s.d);
+  CrossArgs q = a;
+  a.splits = p.dkv_splits;
+  q.splits = p.tc ? p.rounds.splits : p.dq_splits;
+  q.whole = p.rounds.whole;
+  q.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.dq_part);
   cudaError_t e = launch_cross_delta(a, dtype, cs, log);
-  if (e == cudaSuccess && s.Nk > 0) {
-    a.splits = p.dkv_splits;
-    e = p.tc ? launch_cross_tc_dkv(a, err, cs, log) : launch_cross_simt_dkv(a, dtype, cs, log);
-  }
-  if (e == cudaSuccess && !with_q) {
-    CrossArgs q = a;
-    q.splits = p.tc ? p.rounds.splits : p.dq_splits;
-    q.whole = p.rounds.whole;
-    q.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.dq_part);
-    e = p.tc ? launch_cross_tc_dq(q, err, cs, log) : launch_cross_simt_dq(q, dtype, cs, log);
+  if (p.tc) {
+    if (e == cudaSuccess) e = launch_cross_tc_backward(a, q, err, cs, log);
+  } else {
+    if (e == cudaSuccess && s.Nk > 0) e = launch_cross_simt_dkv(a, dtype, cs, log);
+    if (e == cudaSuccess) e = launch_cross_simt_dq(q, dtype, cs, log);
     if (e == cudaSuccess && p.dq_splits > 1) e = launch_partial_sum(dtype, q.part, p.dq_splits, &dQ, 1, qn, cs, log);
   }
   if (e == cudaSuccess && s.Nk > 0 && p.dkv_splits > 1) {

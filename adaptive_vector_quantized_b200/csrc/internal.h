@@ -184,10 +184,11 @@ cudaError_t make_tmap_view_bf16(CUtensorMap* map, const void* base, const Stride
 // Tensor-core kernels of the cross attention (bf16).
 cudaError_t launch_cross_few(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_tc(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
-// With one key tile and d = 64 the first of the two writes dQ as well.
+// With one key tile and d = 64 the kernel of dK and dV writes dQ as well.
 bool cross_tc_dkv_forms_dq(int Nk, int d);
-cudaError_t launch_cross_tc_dkv(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
-cudaError_t launch_cross_tc_dq(const CrossArgs& a, unsigned int* err, cudaStream_t st, LaunchLog& log);
+// dK and dV with a, dQ with q.
+cudaError_t launch_cross_tc_backward(const CrossArgs& a, const CrossArgs& q, unsigned int* err, cudaStream_t st,
+                                     LaunchLog& log);
 
 // Device address of the current device's error word.
 unsigned int* error_word();
