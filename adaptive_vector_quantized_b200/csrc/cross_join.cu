@@ -135,11 +135,21 @@ __global__ void __launch_bounds__(kThreads) partial_sum_kernel(const float* part
   }
 }
 
-// delta[row] = sum_d dO O, one row per d / 8 lanes: dO and O read once.
+// delta[row] = sum_d dO O, one row per d / 8 lanes: dO and O read once.  With a mask a
+// block more for each encoder sequence, which counts the keys that are looked at as
+// far as the second.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_delta_kernel(const CrossArgs a) {
+__global__ void __launch_bounds__(kThreads) cross_delta_kernel(const CrossArgs a, unsigned row_blocks) {
   grid_dependency_wait();
   allow_dependents();
+  if (blockIdx.x >= row_blocks) {
+    const int kb = (int)(blockIdx.x - row_blocks), count = key_count(a, kb);
+    int seen = 0;
+    for (int j = 0; j < count && seen < 2; j += kThreads)
+      seen += __syncthreads_count(key_seen(a, kb, j + (int)threadIdx.x, count));
+    if (threadIdx.x == 0) a.lone[kb] = seen == 1;
+    return;
+  }
   constexpr int L = D / 8;
   const long long rows = (long long)a.B * a.Hq * a.Nq;
   const long long row = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
@@ -219,7 +229,7 @@ cudaError_t launch_cross_delta(const CrossArgs& a, avq_dtype dt, cudaStream_t st
   log.add("cross_delta");
   const auto kernel = dt == AVQ_F32 ? (a.d == 64 ? cross_delta_kernel<float, 64> : cross_delta_kernel<float, 128>)
                                     : (a.d == 64 ? cross_delta_kernel<bf16, 64> : cross_delta_kernel<bf16, 128>);
-  return launch_after(kernel, dim3(grid), dim3(kThreads), 0, st, a);
+  return launch_after(kernel, dim3(grid + (a.lone != nullptr ? a.Bk : 0)), dim3(kThreads), 0, st, a, grid);
 }
 
 }  // namespace avq

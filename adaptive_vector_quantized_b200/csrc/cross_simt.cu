@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
                   [&](int r) { return seen[r] != 0; });
   fetch_tile<T, D>(sV, static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h, a.vs.n, k0,
                   [&](int r) { return seen[r] != 0; });
-  const float c2 = a.scale * kLog2e;
+  const float c2 = a.scale * kLog2e, f = ds_scale(a, kb, count);
   float2 dk[kM][D / 32], dv[kM][D / 32];
   clear(dk);
   clear(dv);
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
     float p[kM][4], ds[kM][4];
     rows_rows<D>(sQ, sK, ty, tx, p);
     rows_rows<D>(sG, sV, ty, tx, ds);
-    scores_back(sL[place], sDelta[place], seen, ty, tx, c2, a.scale, p, ds);
+    scores_back(sL[place], sDelta[place], seen, ty, tx, c2, f, p, ds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
   load_rows(a, sL, sDelta, head_row, row0);
   const T* K = static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h;
   const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
-  const float c2 = a.scale * kLog2e;
+  const float c2 = a.scale * kLog2e, f = ds_scale(a, kb, count);
   float2 dq[kM][D / 32];
   clear(dq);
   for (int t = t0; t < t1; ++t) {
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
     load_tile<T, D>(sKV, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
     __syncthreads();
     rows_rows<D>(sQ, sKV, ty, tx, p);
-    scores_back(sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
+    scores_back(sL, sDelta, seen, ty, tx, c2, f, p, ds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll

@@ -5,7 +5,7 @@
 // order and no gradient passes through memory in fp32.
 //
 //   P = exp(S - lse),  dP = dO V^T,  dS = P (dP - delta),
-//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K  (0 for scale with one key alone).
 //
 // A block has two groups of four warps for the elementwise work (a TMEM lane to
 // a thread, half of the tile's columns to a group), a warp that loads by TMA, one
@@ -464,13 +464,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
     uint32_t steps = 0, dones = 0;
     bool ok = true;
     RowTile before{};  // the row tile of the step before, whose dQ is under way
+    float factor = 0.f;  // on dS K and dS^T Q
     // dQ of step n: its group (they take turns) writes the rows
     auto write_q = [&](uint32_t n) {
       const uint32_t buf = n & 1;
       if (!guard.wait(bar.dq_full + buf, n >> 1 & 1)) return false;
       tc::tc_fence_after();
       if (half == (int)buf) {
-        store_block(tQ + buf * D + lane_off, a.scale, sm + S::kOutQ + warp * 4096, &maps.out2, 0,
+        store_block(tQ + buf * D + lane_off, factor, sm + S::kOutQ + warp * 4096, &maps.out2, 0,
                     before.row0 + quarter * 32, a.Nq, a.Hq > 1 ? before.h : 0, a.B > 1 ? before.b : 0, lane);
         tc::tc_fence_before();
         __syncwarp();
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           }
         }
       }
+      factor = ds_scale(a, x.kb, x.count);
       const int key = x.k0 + quarter * 32 + lane;
       const bool live = key_seen(a, x.kb, key, x.count);
       for (int j = x.i0; j < x.i1; ++j, ++steps) {
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       // group 0 writes dV, group 1 dK
       const bool any = x.i0 < x.i1;
       const uint32_t acc = (half == 0 ? tV : tK) + lane_off;
-      const float f = half == 0 ? 1.f : a.scale;
+      const float f = half == 0 ? 1.f : factor;
       const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
       const size_t at = (((size_t)x.kb * a.Hk + x.kh) * a.Nk + key) * D;
       if (any) {
@@ -866,16 +868,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         tc::tc_fence_after();
       }
       // 64 columns of dQ to a group
+      const float factor = ds_scale(a, x.kb, x.count);
       if (half < S::kBlocks) {
         if (x.parts > 1) {
           float* dst = a.part + ((size_t)(i - a.whole) * 128 + quarter * 32 + lane) * D + half * 64;
           if (any) {
-            store_partial<64>(tQ + lane_off + half * 64, a.scale, dst, in);
+            store_partial<64>(tQ + lane_off + half * 64, factor, dst, in);
           } else if (in) {
             for (int c = 0; c < 64; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
           }
         } else if (any) {
-          store_block(tQ + lane_off + half * 64, a.scale, out, &maps.out0, half * 64, x.row0 + quarter * 32, a.Nq,
+          store_block(tQ + lane_off + half * 64, factor, out, &maps.out0, half * 64, x.row0 + quarter * 32, a.Nq,
                       a.Hq > 1 ? x.h : 0, a.B > 1 ? x.b : 0, lane);
         } else if (in) {
           bf16* dst = static_cast<bf16*>(a.dQ) + at * D + half * 64;

@@ -239,9 +239,9 @@ struct CrossPlan {
   int splits = 1;    // forward, except for tc
   Rounds rounds;     // tc: forward, or dQ
   int dkv_splits = 1, dq_splits = 1;
-  size_t part = 0, part_lse = 0, delta = 0;  // bytes, each a multiple of 256
+  size_t part = 0, part_lse = 0, delta = 0, lone = 0;  // bytes, each a multiple of 256
   size_t dq_part = 0;                        // where dQ's begin in part
-  size_t total() const { return part + part_lse + delta; }
+  size_t total() const { return part + part_lse + delta + lone; }
 };
 
 CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
@@ -276,6 +276,7 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
     return p;
   }
   p.delta = up256((size_t)rows * 4);
+  p.lone = up256((size_t)s.Bk * 4);
   // dQ may be formed while dK and dV are: each in a place of its own
   size_t dq;
   if (p.tc) {
@@ -517,6 +518,7 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   a.dQ = dQ, a.dK = dK, a.dV = dV;
   a.part = static_cast<float*>(ws);
   a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+  if (key_mask != nullptr) a.lone = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.part + p.delta);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   unsigned int* err = error_word();
   if (err == nullptr) return api_fail(AVQ_ERR_CUDA, "cannot resolve the device error word");

@@ -148,6 +148,8 @@ struct CrossArgs {
   float *lse, *delta, *part, *part_lse;
   const int32_t* kv_lens;
   const uint8_t* key_mask;
+  // backward with a mask: whether one key alone is looked at, per encoder sequence
+  int32_t* lone;
 };
 cudaError_t launch_cross_few_f32(const CrossArgs& a, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_simt(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
@@ -164,7 +166,7 @@ cudaError_t launch_cross_join_items(const CrossArgs& a, int items, int per_head,
 // 2), i < n (a multiple of 4).
 cudaError_t launch_partial_sum(avq_dtype dt, const float* part, int splits, void* const* out, int outs, size_t n,
                                cudaStream_t st, LaunchLog& log);
-// delta = rowsum(dO O)
+// delta = rowsum(dO O), and a.lone where it is given
 cudaError_t launch_cross_delta(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
 
 // What the entry points outside avq_api.cu share with it: the thread-local

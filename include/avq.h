@@ -475,8 +475,9 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
  * call, and the O (with strides) and lse that it wrote.
  * Outputs: dQ [B,Hq,Nq,d]; dK, dV [Bk,Hk,Nk,d], summed over the query heads
  * and batch entries that share them; of `dtype`, dense, written in full (keys
- * that are not looked at get 0).  No atomics: results are the same from run
- * to run on one kind of GPU.
+ * that are not looked at get 0).  Of an encoder sequence with one key that is
+ * looked at, dK and the dQ of its rows are 0: its weight is 1 whatever the
+ * score.  No atomics: results are the same from run to run on one kind of GPU.
  * Workspace: avq_cross_workspace_size(dims, dtype, 1) bytes.
  */
 avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dtype, const void* dO,

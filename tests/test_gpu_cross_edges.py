@@ -1,0 +1,61 @@
+"""Exact attention where its arithmetic degenerates: one key to a row, scores
+and inputs that are not finite, gradients of keys that are left out."""
+import pytest
+import torch
+
+import adaptive_vector_quantized_b200 as avq
+from tests import exact_ref as ref
+from tests.test_gpu_cross import DT, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=["bf16", "bf16_cuda_cores", "f32"])
+def family(request):
+    """The element type, on the kernels that it is computed by."""
+    old = avq.avq_set_path(avq.AVQ_PATH_SIMT if request.param == "bf16_cuda_cores" else avq.AVQ_PATH_AUTO)
+    yield DT[request.param.split("_")[0]]
+    avq.avq_set_path(old)
+
+
+# ---- one key -------------------------------------------------------------------------------
+# The softmax over one key is 1 whatever its score, so dQ and dK are 0 by
+# definition: dO V^T and rowsum(dO O) are one number, whose two forms in fp32
+# must not leave their difference behind.
+
+
+# B, Bk, Hq, Hk, Nq, Nk, lens, the keys that a mask leaves of each encoder sequence
+LONE = {
+    "nk_1": (2, 1, 4, 2, 130, 1, None, None),
+    "nk_1_many_rows": (1, 1, 2, 1, 5000, 1, None, None),
+    "lens": (3, 3, 2, 2, 70, 40, [1, 40, 0], None),
+    "mask": (4, 2, 4, 2, 90, 300, None, [[170], [0, 299]]),
+    "mask_and_lens": (2, 2, 2, 2, 33, 500, [260, 500], [[257, 260, 499], [3]]),
+    "mask_one_tile": (2, 2, 2, 2, 200, 77, None, [[76], [0, 76]]),
+    "mask_long": (1, 1, 2, 2, 64, 5000, None, [[4990]]),
+}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", list(LONE))
+def test_one_key_has_no_gradient_through_the_softmax(case, d, family):
+    B, Bk, Hq, Hk, Nq, Nk, lens, seen = LONE[case]
+    Q, K, V, dO, _ = inputs(B, Bk, Hq, Hk, Nq, Nk, d, family, 31)
+    lens = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    mask = None
+    if seen is not None:
+        mask = torch.zeros(Bk, Nk, dtype=torch.bool)
+        for i, keys in enumerate(seen):
+            mask[i, keys] = True
+    kw = dict(kv_lens=None if lens is None else lens.cuda(), key_mask=None if mask is None else mask.cuda())
+    O, lse = avq.avq_cross_attention(Q, K, V, lse=True, **kw)
+    grads = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse, **kw)
+    want = ref.cross(Q, K, V, lens, mask, dO=dO, O_given=O)
+    for n, t in zip(("dQ", "dK", "dV"), grads):
+        ref.check(n, t, want[n], want[n + "_tol"] * 2)  # lse as the kernel wrote it
+    alone = ref.keep_mask(Bk, Nk, lens, mask).sum(1) == 1
+    assert alone.any()
+    assert (grads[0].cpu()[alone.repeat_interleave(B // Bk)] == 0).all()
+    assert (grads[1].cpu()[alone] == 0).all()
+    if not alone.all() and case != "lens":
+        assert (grads[0].cpu()[~alone.repeat_interleave(B // Bk)] != 0).any()
