@@ -5,12 +5,16 @@
 // Linear: positions interpolated, every frequency / factor.  NTK: the base
 // raised so that the slowest pair (i = p - 1) is divided by factor and the
 // fastest kept.  YaRN ("YaRN: Efficient Context Window Extension of Large
-// Language Models", Sec. 3): pair i makes trained * f / (2 pi) turns over the
-// trained range; the pair index at which that number is r is
-// p ln(trained / (2 pi r)) / ln(base).  Below the (rounded down) index of
-// turns_high frequencies are kept, above the (rounded up) index of turns_low
-// they are divided by factor, with a linear ramp between; the logits'
-// temperature goes into mscale = 0.1 ln(factor) + 1.
+// Language Models"): pair i makes trained * f / (2 pi) turns over the trained
+// range; the pair index at which that number is r is
+// p ln(trained / (2 pi r)) / ln(base).  Up to the (rounded down) index of
+// turns_high frequencies are kept, from the (rounded up) index of turns_low on
+// they are divided by factor, with a ramp between; the logits' temperature goes
+// into mscale = 0.1 ln(factor) + 1.  The ramp is linear in the pair index, as in
+// the published code; the paper's Sec. 3 writes it linear in turns.  Like that code's it
+// begins at pair 0 or later and ends at 2 p - 1, the rotated elements of an axis
+// less one, or earlier: past the last pair where that one still makes more than
+// turns_low turns.  Where even pair 0 makes fewer, all are divided.
 #include <math.h>
 
 #include "internal.h"
@@ -34,16 +38,18 @@ extern "C" avq_status avq_rotary_freqs(int rot, int axes, double base, avq_rotar
   const int pairs = rot / 2 / axes;
   if (scaling == AVQ_ROTARY_NTK) base *= pow(factor, (double)pairs / (pairs - 1));
   const double two_pi = 6.283185307179586477;
-  double lo = 0.0, hi = 0.0;
+  double kept = 0.0, divided = 0.0;  // pair indexes, not confined to the pairs
   if (scaling == AVQ_ROTARY_YARN) {
-    lo = fmax(floor(pairs * log(trained / (two_pi * turns_high)) / log(base)), 0.0);
-    hi = fmin(ceil(pairs * log(trained / (two_pi * turns_low)) / log(base)), pairs - 1.0);
+    kept = floor(pairs * log(trained / (two_pi * turns_high)) / log(base));
+    divided = ceil(pairs * log(trained / (two_pi * turns_low)) / log(base));
   }
+  const double lo = fmax(kept, 0.0), hi = fmin(divided, 2.0 * pairs - 1.0);  // the ramp's ends
   for (int i = 0; i < pairs; ++i) {
     double f = pow(base, -(double)i / pairs);
     if (scaling == AVQ_ROTARY_LINEAR) f /= factor;
     if (scaling == AVQ_ROTARY_YARN) {
-      const double ramp = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+      // between kept and divided lo <= i < hi
+      const double ramp = i >= divided ? 1.0 : i <= kept ? 0.0 : (i - lo) / (hi - lo);
       f *= (1.0 - ramp) + ramp / factor;
     }
     for (int ax = 0; ax < axes; ++ax) freqs[ax * pairs + i] = f;
