@@ -24,7 +24,8 @@
 //
 // Bound by the exponentials at d = 64 (16 a clock and SM), by them and the
 // tensor pipe alike at d = 128; so a quarter of them go to the FMA pipe
-// (fm::exp2_poly2, 7.5e-5 relative, a fiftieth of P's rounding).
+// (fm::exp2_poly2, 7.5e-5 relative, a fiftieth of P's rounding).  Scores that are
+// not finite go by the row's maximum, not by that exponential.
 #include "cross_tc.cuh"
 
 namespace avq {
@@ -447,7 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       }
       if (!ok) break;
       if (end - first > kStep) tail_phase ^= 1;
-      const float z = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      float z = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      // The FMA pipe's exponential is 2^-126 at least, and hides a NaN.  A NaN score
+      // is in the sum all the same (the whole row's exponents are NaN then); what is
+      // left are a score of +inf, whose row is NaN, and rows of -inf alone.
+      if (m == INFINITY) z = NAN;
+      if (m == -INFINITY) z = 0.f;
       const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : z);
       const float lse = z == 0.f ? -INFINITY : a.scale * m + logf(z);
       const bool any = x.t0 < x.t1;

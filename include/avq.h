@@ -454,8 +454,9 @@ typedef struct {
  * Looked at are the keys below kv_lens[kb] (int32 [Bk], NULL: Nk; values
  * outside [0, Nk] are taken as the nearer end) whose key_mask byte (uint8
  * [Bk,Nk], NULL: all) is not 0.  What stands in the others' K and V does not
- * matter, infinities and NaN included.  A row with no key gives O = 0 and
- * lse = -inf.
+ * matter, infinities and NaN included.  A row with no key, or with scores of
+ * -inf alone, gives O = 0 and lse = -inf; one with a score of NaN or +inf
+ * gives NaN.
  * Outputs (device): O [B,Hq,Nq,d] of `dtype` with strides; lse fp32
  * [B,Hq,Nq], dense, or NULL.  O and lse overlap no input and not each other;
  * O's strides let no two rows overlap.

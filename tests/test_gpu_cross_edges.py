@@ -59,3 +59,43 @@ def test_one_key_has_no_gradient_through_the_softmax(case, d, family):
     assert (grads[1].cpu()[alone] == 0).all()
     if not alone.all() and case != "lens":
         assert (grads[0].cpu()[~alone.repeat_interleave(B // Bk)] != 0).any()
+
+
+# ---- scores that are not finite --------------------------------------------------------------
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("Nq", [3, 200])
+@pytest.mark.parametrize("key", [*range(8), 131, 134, 255])
+def test_an_infinite_score_is_not_hidden(key, Nq, masked, family):
+    """exp(inf - inf): every row that sees the key is NaN, the other heads are as they were."""
+    Q, K, V, _, _ = inputs(1, 1, 2, 2, Nq, 256, 64, family, 32)
+    Q[..., 0] = 1.0
+    mask = None
+    if masked:
+        mask = torch.ones(1, 256, dtype=torch.bool, device="cuda")
+        mask[0, [11, 140]] = False
+    want, wl = avq.avq_cross_attention(Q, K, V, key_mask=mask, lse=True)
+    K[0, 1, key, 0] = float("inf")
+    O, lse = avq.avq_cross_attention(Q, K, V, key_mask=mask, lse=True)
+    assert torch.isnan(O[0, 1]).all() and torch.isnan(lse[0, 1]).all()
+    assert torch.equal(O[0, 0], want[0, 0]) and torch.equal(lse[0, 0], wl[0, 0])
+
+
+@pytest.mark.parametrize("Nq", [3, 200])
+@pytest.mark.parametrize("Nk", [64, 256, 700, 5000])
+def test_scores_of_minus_infinity_weigh_nothing(Nk, Nq, family):
+    """All of a row's: as a row without keys.  Those of its first keys: as if they were left out."""
+    Q, K, V, _, _ = inputs(1, 1, 2, 2, Nq, Nk, 64, family, 33)
+    Q[..., 0] = 1e25  # finite: the product overflows
+    K[..., 0] = 0.0
+    K[0, 0, :, 0] = -1e25
+    first = Nk // 2 + 1
+    K[0, 1, :first, 0] = -1e25
+    O, lse = avq.avq_cross_attention(Q, K, V, lse=True)
+    assert (O[0, 0] == 0).all() and (lse[0, 0] == float("-inf")).all()
+    Q[..., 0] = 0.0
+    rest = torch.arange(Nk, device="cuda")[None] >= first
+    want = ref.cross(Q, K, V, key_mask=rest)
+    ref.check("O", O[:, 1:], want["O"][:, 1:], want["O_tol"][:, 1:])
+    ref.check("lse", lse[:, 1:], want["lse"][:, 1:], want["lse_tol"][:, 1:])
