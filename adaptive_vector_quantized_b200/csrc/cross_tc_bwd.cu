@@ -163,14 +163,17 @@ __device__ __forceinline__ void mma_tmem_cols(uint32_t d, uint32_t a, uint64_t b
 }
 constexpr int kHalf16 = 64 * 128 >> 4;  // from a tile's row 0 to its row 64, in units of a descriptor
 
-// p = exp2(c2 s + nl) for 32 scores; packed to bf16 in out
+// -log2e lse of a row; one with scores of -inf alone has lse = -inf and P = 0.
+__device__ __forceinline__ float row_shift(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+
+// p = exp2(c2 s + nl) for 32 scores, a quarter of them on the FMA pipe
 template <bool kVec>
 __device__ __forceinline__ void exp_chunk(const uint32_t* r, float2 c2, const float* nl, float2 nl1, float2* p) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float2 l = kVec ? fm::f2(nl[2 * i], nl[2 * i + 1]) : nl1;
     const float2 x = fm::fma2(fm::f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), c2, l);
-    p[i] = (i & 3) == 3 ? fm::exp2_poly2(x) : fm::f2(tc::ex2(x.x), tc::ex2(x.y));
+    p[i] = (i & 3) == 3 ? fm::exp2_poly2_any(x) : fm::f2(tc::ex2(x.x), tc::ex2(x.y));
   }
 }
 
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           for (int e = 0; e < 4; ++e) {
             const int row = r.row0 + 32 * e + lane;
             const bool in = row < a.Nq;  // past the end: P = exp2(-inf)
-            l[e] = in ? -__ldg(a.lse + head + row) * kLog2e : -INFINITY;
+            l[e] = in ? row_shift(__ldg(a.lse + head + row)) : -INFINITY;
             d[e] = in ? -__ldg(a.delta + head + row) : 0.f;
           }
           ok = guard.wait(bar.rows_empty + (n & 1), (n >> 1 & 1) ^ 1);
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
       const int row = x.row0 + quarter * 32 + lane;
       const size_t at = ((size_t)x.b * a.Hq + x.h) * a.Nq + row;
       const bool in = row < a.Nq;
-      const float l = in ? -__ldg(a.lse + at) * kLog2e : -INFINITY;
+      const float l = in ? row_shift(__ldg(a.lse + at)) : -INFINITY;
       const float dl = in ? -__ldg(a.delta + at) : 0.f;
       const float2 nl = fm::f2(l, l), nd = fm::f2(dl, dl);
       for (int j = x.t0; j < x.t1; ++j, ++steps) {

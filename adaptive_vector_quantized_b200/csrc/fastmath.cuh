@@ -29,6 +29,17 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
+// x = j + f as below, j behind the rounding constant; returns 2^f.
+__device__ __forceinline__ float2 exp2_parts(float2 x, float2* j) {
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+  *j = add2(x, f2(kRound, kRound));
+  const float2 jf = add2(*j, f2(-kRound, -kRound));
+  const float2 f = add2(x, f2(-jf.x, -jf.y));
+  float2 p = fma2(f2(0.05517166493f, 0.05517166493f), f, f2(0.24261112188f, 0.24261112188f));
+  p = fma2(p, f, f2(0.69326098622f, 0.69326098622f));
+  return fma2(p, f, f2(0.99992807358f, 0.99992807358f));
+}
+
 // 2^x for two values on the FMA pipe instead of the special-function unit.
 // Range reduction to the nearest integer (Cody and Waite): j = round(x) by
 // adding and subtracting 1.5 * 2^23 (exact round-to-nearest for |x| < 2^22),
@@ -41,18 +52,24 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // 2^f >= 2^-1/2 keep it at 0 or above: a non-negative number below 2^-125);
 // inputs must stay below 127.5.
 __device__ __forceinline__ float2 exp2_poly2(float2 x) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
-  x.x = fmaxf(x.x, -126.0f);
-  x.y = fmaxf(x.y, -126.0f);
-  const float2 j = add2(x, f2(kRound, kRound));
-  const float2 jf = add2(j, f2(-kRound, -kRound));
-  const float2 f = add2(x, f2(-jf.x, -jf.y));
-  float2 p = fma2(f2(0.05517166493f, 0.05517166493f), f, f2(0.24261112188f, 0.24261112188f));
-  p = fma2(p, f, f2(0.69326098622f, 0.69326098622f));
-  p = fma2(p, f, f2(0.99992807358f, 0.99992807358f));
+  float2 j;
+  const float2 p = exp2_parts(f2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f)), &j);
   const uint32_t r0 = __float_as_uint(p.x) + (__float_as_uint(j.x) << 23);
   const uint32_t r1 = __float_as_uint(p.y) + (__float_as_uint(j.y) << 23);
   return f2(__uint_as_float(r0), __uint_as_float(r1));
+}
+
+// The same for any input below 127.5: NaN stays NaN, and below -126.5 the result is 0.
+// 2^j is a factor here, made from j as its exponent field (of j = -127: 0), since an
+// addition to the bits of a NaN gives a finite number: one packed product more.
+__device__ __forceinline__ float2 exp2_poly2_any(float2 x) {
+  float2 j;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.0f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.0f));
+  const float2 p = exp2_parts(x, &j);
+  const uint32_t e0 = (__float_as_uint(j.x) << 23) + 0x3f800000u;
+  const uint32_t e1 = (__float_as_uint(j.y) << 23) + 0x3f800000u;
+  return mul2(p, f2(__uint_as_float(e0), __uint_as_float(e1)));
 }
 
 // tcgen05.ld of shape 16x256b, 4 repetitions: 16 TMEM lanes x 32 columns.

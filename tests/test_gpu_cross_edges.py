@@ -99,3 +99,46 @@ def test_scores_of_minus_infinity_weigh_nothing(Nk, Nq, family):
     want = ref.cross(Q, K, V, key_mask=rest)
     ref.check("O", O[:, 1:], want["O"][:, 1:], want["O_tol"][:, 1:])
     ref.check("lse", lse[:, 1:], want["lse"][:, 1:], want["lse_tol"][:, 1:])
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("Nk, d", [(77, 64), (300, 64), (300, 128)])
+@pytest.mark.parametrize("row", [*range(8), 134, 199])
+def test_a_nan_query_reaches_every_gradient(row, Nk, d, masked, family):
+    """Of its row's dQ, and of dK and dV of every key that the row sees; nothing else changes."""
+    Q, K, V, dO, _ = inputs(1, 1, 2, 2, 200, Nk, d, family, 34)
+    mask = None
+    if masked:
+        mask = torch.ones(1, Nk, dtype=torch.bool, device="cuda")
+        mask[0, [5, 70]] = False
+    O, lse = avq.avq_cross_attention(Q, K, V, key_mask=mask, lse=True)
+    want = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse, key_mask=mask)
+    Q[0, 1, row, 7] = float("nan")
+    O, lse = avq.avq_cross_attention(Q, K, V, key_mask=mask, lse=True)
+    dQ, dK, dV = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse, key_mask=mask)
+    seen = slice(None) if mask is None else mask[0]
+    for n, t in (("dK", dK), ("dV", dV)):
+        assert torch.isnan(t[0, 1][seen]).all(), n
+    rows = torch.arange(200, device="cuda") != row
+    assert torch.isnan(dQ[0, 1, row]).all() and torch.equal(dQ[0, 1, rows], want[0][0, 1, rows])
+    assert all(torch.equal(a[0, 0], b[0, 0]) for a, b in zip((dQ, dK, dV), want))
+
+
+@pytest.mark.parametrize("Nk, d", [(77, 64), (128, 128), (300, 64), (300, 128)])
+def test_scores_of_minus_infinity_have_no_gradient(Nk, d, family):
+    """A row all of whose scores are -inf has no part in any gradient."""
+    Q, K, V, dO, _ = inputs(1, 1, 2, 2, 200, Nk, d, family, 35)
+    Q[..., 0] = 0.0
+    K[..., 0] = 1e25
+    rows = torch.tensor([0, 3, 6, 7, 134, 199])
+    Q[0, 1, rows, 0] = -1e25
+    O, lse = avq.avq_cross_attention(Q, K, V, lse=True)
+    assert (lse[0, 1, rows] == float("-inf")).all()
+    dQ, dK, dV = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse)
+    assert (dQ[0, 1, rows] == 0).all()
+    others = torch.ones(200, dtype=torch.bool)
+    others[rows] = False
+    want = ref.cross(Q[:, 1:, others], K[:, 1:], V[:, 1:], dO=dO[:, 1:, others], O_given=O[:, 1:, others])
+    ref.check("dQ", dQ[:, 1:, others], want["dQ"], want["dQ_tol"] * 2)
+    ref.check("dK", dK[:, 1:], want["dK"], want["dK_tol"] * 2)
+    ref.check("dV", dV[:, 1:], want["dV"], want["dV_tol"] * 2)
