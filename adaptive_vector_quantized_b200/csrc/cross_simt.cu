@@ -373,8 +373,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
     const size_t at = (((size_t)kb * a.Hk + kh) * a.Nk + r) * D;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const float k4[4] = {dk[i][2 * c].x, dk[i][2 * c].y, dk[i][2 * c + 1].x, dk[i][2 * c + 1].y};
-      const float v4[4] = {dv[i][2 * c].x, dv[i][2 * c].y, dv[i][2 * c + 1].x, dv[i][2 * c + 1].y};
+      float k4[4] = {dk[i][2 * c].x, dk[i][2 * c].y, dk[i][2 * c + 1].x, dk[i][2 * c + 1].y};
+      float v4[4] = {dv[i][2 * c].x, dv[i][2 * c].y, dv[i][2 * c + 1].x, dv[i][2 * c + 1].y};
+      if (!seen[kM * ty + i]) {  // whatever the rows held
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k4[e] = v4[e] = 0.f;
+      }
       if (a.splits > 1) {
         put4(a.part + (size_t)split * 2 * elems + at + 4 * tx + 64 * c, k4);
         put4(a.part + ((size_t)split * 2 + 1) * elems + at + 4 * tx + 64 * c, v4);

@@ -177,9 +177,10 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* r, float2 c2, const fl
   }
 }
 
-// 64 columns of an accumulator row (times f), as bf16 into the warp's staging
-// rows, then to memory by TMA.
-__device__ __forceinline__ void store_block(uint32_t taddr, float f, uint8_t* out, const CUtensorMap* map, int col,
+// 64 columns of an accumulator row (times f; 0 for a key that is left out, `on`
+// false, whatever the rows held), as bf16 into the warp's staging rows, then to
+// memory by TMA.
+__device__ __forceinline__ void store_block(uint32_t taddr, float f, bool on, uint8_t* out, const CUtensorMap* map, int col,
                                             int row, int rows, int h, int b, int lane) {
   if (lane == 0) tc::bulk_wait_group_read0();
   __syncwarp();
@@ -188,6 +189,10 @@ __device__ __forceinline__ void store_block(uint32_t taddr, float f, uint8_t* ou
     uint32_t o[32];
     tc::tmem_ld32(taddr + c * 32, o);
     tc::tmem_wait_ld();
+    if (!on) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = 0u;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint4 v;
@@ -207,12 +212,16 @@ __device__ __forceinline__ void store_block(uint32_t taddr, float f, uint8_t* ou
 }
 // The same row in fp32, straight to memory (partial results).
 template <int D>
-__device__ __forceinline__ void store_partial(uint32_t taddr, float f, float* dst, bool live) {
+__device__ __forceinline__ void store_partial(uint32_t taddr, float f, bool on, float* dst, bool live) {
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     uint32_t o[16];
     tc::tmem_ld16(taddr + c * 16, o);
     tc::tmem_wait_ld();
+    if (!on) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[k] = 0u;
+    }
     if (live) {
 #pragma unroll
       for (int k = 0; k < 16; k += 4)
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       if (!guard.wait(bar.dq_full + buf, n >> 1 & 1)) return false;
       tc::tc_fence_after();
       if (half == (int)buf) {
-        store_block(tQ + buf * D + lane_off, factor, sm + S::kOutQ + warp * 4096, &maps.out2, 0,
+        store_block(tQ + buf * D + lane_off, factor, true, sm + S::kOutQ + warp * 4096, &maps.out2, 0,
                     before.row0 + quarter * 32, a.Nq, a.Hq > 1 ? before.h : 0, a.B > 1 ? before.b : 0, lane);
         tc::tc_fence_before();
         __syncwarp();
@@ -595,14 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       if (a.splits > 1) {
         float* dst = a.part + ((size_t)x.split * 2 + (half == 0 ? 1 : 0)) * elems + at;
         if (any) {
-          store_partial<D>(acc, f, dst, key < a.Nk);
+          store_partial<D>(acc, f, live, dst, key < a.Nk);
         } else if (key < a.Nk) {
           for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       } else if (any) {
 #pragma unroll
         for (int cb = 0; cb < S::kBlocks; ++cb)
-          store_block(acc + cb * 64, f, out, half == 0 ? &maps.out0 : &maps.out1, cb * 64, x.k0 + quarter * 32, a.Nk,
+          store_block(acc + cb * 64, f, live, out, half == 0 ? &maps.out0 : &maps.out1, cb * 64, x.k0 + quarter * 32, a.Nk,
                       a.Hk > 1 ? x.kh : 0, a.Bk > 1 ? x.kb : 0, lane);
       } else if (key < a.Nk) {
         bf16* dst = static_cast<bf16*>(half == 0 ? a.dV : a.dK) + at;
@@ -876,12 +885,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         if (x.parts > 1) {
           float* dst = a.part + ((size_t)(i - a.whole) * 128 + quarter * 32 + lane) * D + half * 64;
           if (any) {
-            store_partial<64>(tQ + lane_off + half * 64, factor, dst, in);
+            store_partial<64>(tQ + lane_off + half * 64, factor, true, dst, in);
           } else if (in) {
             for (int c = 0; c < 64; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
           }
         } else if (any) {
-          store_block(tQ + lane_off + half * 64, factor, out, &maps.out0, half * 64, x.row0 + quarter * 32, a.Nq,
+          store_block(tQ + lane_off + half * 64, factor, true, out, &maps.out0, half * 64, x.row0 + quarter * 32, a.Nq,
                       a.Hq > 1 ? x.h : 0, a.B > 1 ? x.b : 0, lane);
         } else if (in) {
           bf16* dst = static_cast<bf16*>(a.dQ) + at * D + half * 64;

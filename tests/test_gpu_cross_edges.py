@@ -142,3 +142,23 @@ def test_scores_of_minus_infinity_have_no_gradient(Nk, d, family):
     ref.check("dQ", dQ[:, 1:, others], want["dQ"], want["dQ_tol"] * 2)
     ref.check("dK", dK[:, 1:], want["dK"], want["dK_tol"] * 2)
     ref.check("dV", dV[:, 1:], want["dV"], want["dV_tol"] * 2)
+
+
+# ---- keys that are left out ------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("Nk, d", [(77, 64), (300, 64), (300, 128)])
+def test_keys_left_out_get_zero_whatever_the_rows_hold(Nk, d, family):
+    Q, K, V, dO, _ = inputs(2, 2, 2, 1, 200, Nk, d, family, 36)
+    lens = torch.tensor([Nk - 9, Nk], dtype=torch.int32, device="cuda")
+    mask = torch.ones(2, Nk, dtype=torch.bool, device="cuda")
+    mask[1, [0, 33, 70]] = False
+    keep = ref.keep_mask(2, Nk, lens, mask)
+    O, lse = avq.avq_cross_attention(Q, K, V, kv_lens=lens, key_mask=mask, lse=True)
+    Q[:, 0, 100, 3] = float("nan")
+    dO[:, 1, 150, 5] = float("inf")
+    _, dK, dV = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse, kv_lens=lens, key_mask=mask)
+    for t in (dK, dV):
+        out = t.cpu()[:, 0]
+        assert (out[~keep] == 0).all()
+        assert not torch.isfinite(out[keep]).all(-1).any()
