@@ -24,12 +24,11 @@ __device__ __forceinline__ bool key_seen(const CrossArgs& a, int kb, int j, int 
   return j < count && (a.key_mask == nullptr || __ldg(a.key_mask + (size_t)kb * a.Nk + j) != 0);
 }
 
-// The factor on dS.  Where one key alone is looked at, P is 1 whatever the score:
-// O is that key's V, dP and delta are the same number, and dS is 0.  Formed in two
-// orders they differ by their roundings, which must not be handed on as a gradient.
-__device__ __forceinline__ float ds_scale(const CrossArgs& a, int kb, int count) {
-  const bool lone = a.lone != nullptr ? a.lone[kb] != 0 : count == 1;
-  return lone ? 0.f : a.scale;
+// Whether one key alone is looked at.  P is 1 then whatever the score: O is that key's
+// V, dP and delta are the same number, and dS, dQ and dK are 0.  Formed in two orders
+// they differ by their roundings, which must not be handed on as a gradient.
+__device__ __forceinline__ bool lone_key(const CrossArgs& a, int kb, int count) {
+  return a.lone != nullptr ? a.lone[kb] != 0 : count == 1;
 }
 
 // Row r of the rows that read encoder sequence kb and key head kh.

@@ -22,7 +22,7 @@
 // and dV the next step's rows beside this one's (in dQ V and K take one place, one
 // after the other, so that another block of the SM covers them).  24 heads of 1000
 // rows and keys of 128: 411 us (30 TFLOP/s; 463 with K and V in one place, 549 with
-// loads that nothing covers), gradients 1.35 ms (1.39 without the next rows).  8 x 4
+// loads that nothing covers), gradients 1.39 ms.  8 x 4
 // scores a thread, with half the threads: 511 us where 4 x 4 took 463, as too few
 // warps are left to cover anything.
 #include "cross.cuh"
@@ -295,11 +295,9 @@ __device__ __forceinline__ void load_rows(const CrossArgs& a, float* sL, float* 
 template <int D>
 constexpr int kRowBufs = D == 64 ? 1 : 2;
 
+// block, split: of the key tiles and of their ranges of rows
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kernel(const CrossArgs a) {
-  grid_dependency_wait();  // delta
-  allow_dependents();      // dQ's blocks may take the places that these leave
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void form_dkv(float* sm, const CrossArgs& a, int block, int split) {
   float* sK = sm;
   float* sV = sK + kT * D;
   constexpr int N = kRowBufs<D>;
@@ -309,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
   __shared__ float sL[N][kT], sDelta[N][kT];
   __shared__ unsigned char seen[kT];
   const int tiles = (a.Nk + kT - 1) / kT;
-  const int kt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
+  const int kt = block % tiles, bh = block / tiles;
   const int kb = bh / a.Hk, kh = bh % a.Hk;
   const int R = a.per_b, G = a.per_h;
   const int k0 = kt * kT;
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
                   [&](int r) { return seen[r] != 0; });
   fetch_tile<T, D>(sV, static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h, a.vs.n, k0,
                   [&](int r) { return seen[r] != 0; });
-  const float c2 = a.scale * kLog2e, f = ds_scale(a, kb, count);
+  const float c2 = a.scale * kLog2e;
   float2 dk[kM][D / 32], dv[kM][D / 32];
   clear(dk);
   clear(dv);
@@ -352,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
     float p[kM][4], ds[kM][4];
     rows_rows<D>(sQ, sK, ty, tx, p);
     rows_rows<D>(sG, sV, ty, tx, ds);
-    scores_back(sL[place], sDelta[place], seen, ty, tx, c2, f, p, ds);
+    scores_back(sL[place], sDelta[place], seen, ty, tx, c2, a.scale, p, ds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -366,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
   }
   tc::cp_async_wait<0>();  // without steps K and V are still under way
   const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
+  const bool lone = lone_key(a, kb, count);
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
     const int r = k0 + kM * ty + i;
@@ -379,6 +378,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
 #pragma unroll
         for (int e = 0; e < 4; ++e) k4[e] = v4[e] = 0.f;
       }
+      if (lone) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k4[e] *= 0.f;  // NaN stays
+      }
       if (a.splits > 1) {
         put4(a.part + (size_t)split * 2 * elems + at + 4 * tx + 64 * c, k4);
         put4(a.part + ((size_t)split * 2 + 1) * elems + at + 4 * tx + 64 * c, v4);
@@ -390,9 +393,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_simt_dkv_kern
   }
 }
 
+// block, split: of the row tiles and of their ranges of keys
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossArgs a) {
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void form_dq(float* sm, const CrossArgs& a, int block, int split) {
   float* sKV = sm;  // V, then K
   float* sQ = sKV + kT * D;
   float* sG = sQ + kT * D;
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
   __shared__ float sL[kT], sDelta[kT];
   __shared__ unsigned char seen[kT];
   const int tiles = (a.Nq + kT - 1) / kT;
-  const int rt = blockIdx.x % tiles, bh = blockIdx.x / tiles, split = blockIdx.y;
+  const int rt = block % tiles, bh = block / tiles;
   const int b = bh / a.Hq, h = bh % a.Hq;
   const int kb = b / a.per_b, kh = h / a.per_h;
   const int row0 = rt * kT;
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
   load_rows(a, sL, sDelta, head_row, row0);
   const T* K = static_cast<const T*>(a.K) + kb * a.ks.b + kh * a.ks.h;
   const T* V = static_cast<const T*>(a.V) + kb * a.vs.b + kh * a.vs.h;
-  const float c2 = a.scale * kLog2e, f = ds_scale(a, kb, count);
+  const float c2 = a.scale * kLog2e;
   float2 dq[kM][D / 32];
   clear(dq);
   for (int t = t0; t < t1; ++t) {
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
     load_tile<T, D>(sKV, K, a.ks.n, k0, [&](int r) { return seen[r] != 0; });
     __syncthreads();
     rows_rows<D>(sQ, sKV, ty, tx, p);
-    scores_back(sL, sDelta, seen, ty, tx, c2, f, p, ds);
+    scores_back(sL, sDelta, seen, ty, tx, c2, a.scale, p, ds);
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
@@ -440,13 +443,18 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
     __syncthreads();
     rows_cols<D>(sD, sKV, ty, tx, dq);
   }
+  const bool lone = lone_key(a, kb, count);
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
     const int r = row0 + ty + 16 * i;
     if (r >= a.Nq) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-      const float v[4] = {dq[i][2 * c].x, dq[i][2 * c].y, dq[i][2 * c + 1].x, dq[i][2 * c + 1].y};
+      float v[4] = {dq[i][2 * c].x, dq[i][2 * c].y, dq[i][2 * c + 1].x, dq[i][2 * c + 1].y};
+      if (lone) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= 0.f;  // NaN stays
+      }
       const size_t at = (head_row + r) * D + 4 * tx + 64 * c;
       if (a.splits > 1)
         put4(a.part + (size_t)split * a.B * a.Hq * a.Nq * D + at, v);
@@ -454,7 +462,39 @@ __global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossA
         put4(static_cast<T*>(a.dQ) + at, v);
     }
   }
-  grid_dependency_wait();  // whatever comes after this kernel comes after dK's and dV's too
+}
+
+// d = 64: the first `keys` blocks form dK and dV (key_tiles of them to a split), the
+// others dQ with the arguments q (row_tiles to a split), on the places that those
+// leave.  One launch, since a kernel for dQ that started beside the other would read
+// delta before its own wait for the work before it, and nothing else makes another
+// kernel's writes visible.  12 heads of 1001 rows over 333 keys: 96 us, 134 with a
+// launch for each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) cross_simt_backward_kernel(const CrossArgs a, const CrossArgs q,
+                                                                         int key_tiles, int keys, int row_tiles) {
+  grid_dependency_wait();
+  extern __shared__ __align__(16) float sm[];
+  const int block = blockIdx.x;
+  if (block < keys)
+    form_dkv<T, 64>(sm, a, block % key_tiles, block / key_tiles);
+  else
+    form_dq<T, 64>(sm, q, (block - keys) % row_tiles, (block - keys) / row_tiles);
+}
+// d = 128: dK and dV take all of an SM's shared memory, dQ half of it, so that one
+// launch would leave dQ one block an SM: a launch for each.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) cross_simt_dkv_kernel(const CrossArgs a) {
+  grid_dependency_wait();
+  allow_dependents();
+  extern __shared__ __align__(16) float sm[];
+  form_dkv<T, 128>(sm, a, blockIdx.x, blockIdx.y);
+}
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) cross_simt_dq_kernel(const CrossArgs a) {
+  grid_dependency_wait();
+  extern __shared__ __align__(16) float sm[];
+  form_dq<T, 128>(sm, a, blockIdx.x, blockIdx.y);
 }
 
 template <typename T, int D>
@@ -466,21 +506,33 @@ cudaError_t forward(const CrossArgs& a, cudaStream_t st) {
   return launch_after(cross_simt_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
 }
 template <typename T, int D>
-cudaError_t dkv(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)((2 + 2 * kRowBufs<D>) * kT * D + 2 * kT * kT) * sizeof(float);
-  cudaError_t e = allow_smem<cross_simt_dkv_kernel<T, D>>((int)smem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT)), a.splits);
-  return launch_after(cross_simt_dkv_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
-}
-template <typename T, int D>
-cudaError_t dq(const CrossArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(3 * kT * D + kT * kT) * sizeof(float);
-  cudaError_t e = allow_smem<cross_simt_dq_kernel<T, D>>((int)smem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT)), a.splits);
-  // dK and dV's kernel waited for delta and writes nothing that is read here
-  return launch_after(cross_simt_dq_kernel<T, D>, grid, dim3(kThreads), smem, st, a);
+cudaError_t backward(const CrossArgs& a, const CrossArgs& q, cudaStream_t st, LaunchLog& log) {
+  const int dkv_smem = ((2 + 2 * kRowBufs<D>) * kT * D + 2 * kT * kT) * (int)sizeof(float);
+  const int dq_smem = (3 * kT * D + kT * kT) * (int)sizeof(float);
+  const unsigned key_tiles = (unsigned)((long long)a.Bk * a.Hk * ((a.Nk + kT - 1) / kT));
+  const unsigned row_tiles = (unsigned)((long long)a.B * a.Hq * ((a.Nq + kT - 1) / kT));
+  cudaError_t e;
+  if constexpr (D == 64) {
+    static_assert(kRowBufs<64> == 1, "dK and dV take more shared memory than dQ");
+    log.add("cross_simt_backward");
+    e = allow_smem<cross_simt_backward_kernel<T>>(dkv_smem);
+    if (e != cudaSuccess) return e;
+    const unsigned keys = key_tiles * a.splits;
+    return launch_after(cross_simt_backward_kernel<T>, dim3(keys + row_tiles * q.splits), dim3(kThreads), dkv_smem,
+                        st, a, q, (int)(key_tiles > 0 ? key_tiles : 1), (int)keys, (int)row_tiles);
+  } else {
+    if (key_tiles > 0) {
+      log.add("cross_simt_dkv");
+      e = allow_smem<cross_simt_dkv_kernel<T>>(dkv_smem);
+      if (e == cudaSuccess)
+        e = launch_after(cross_simt_dkv_kernel<T>, dim3(key_tiles, a.splits), dim3(kThreads), dkv_smem, st, a);
+      if (e != cudaSuccess) return e;
+    }
+    log.add("cross_simt_dq");
+    e = allow_smem<cross_simt_dq_kernel<T>>(dq_smem);
+    if (e != cudaSuccess) return e;
+    return launch_after(cross_simt_dq_kernel<T>, dim3(row_tiles, q.splits), dim3(kThreads), dq_smem, st, q);
+  }
 }
 
 }  // namespace
@@ -490,15 +542,10 @@ cudaError_t launch_cross_simt(const CrossArgs& a, avq_dtype dt, cudaStream_t st,
   if (dt == AVQ_F32) return a.d == 64 ? forward<float, 64>(a, st) : forward<float, 128>(a, st);
   return a.d == 64 ? forward<bf16, 64>(a, st) : forward<bf16, 128>(a, st);
 }
-cudaError_t launch_cross_simt_dkv(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log) {
-  log.add("cross_simt_dkv");
-  if (dt == AVQ_F32) return a.d == 64 ? dkv<float, 64>(a, st) : dkv<float, 128>(a, st);
-  return a.d == 64 ? dkv<bf16, 64>(a, st) : dkv<bf16, 128>(a, st);
-}
-cudaError_t launch_cross_simt_dq(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log) {
-  log.add("cross_simt_dq");
-  if (dt == AVQ_F32) return a.d == 64 ? dq<float, 64>(a, st) : dq<float, 128>(a, st);
-  return a.d == 64 ? dq<bf16, 64>(a, st) : dq<bf16, 128>(a, st);
+cudaError_t launch_cross_simt_backward(const CrossArgs& a, const CrossArgs& q, avq_dtype dt, cudaStream_t st,
+                                       LaunchLog& log) {
+  if (dt == AVQ_F32) return a.d == 64 ? backward<float, 64>(a, q, st, log) : backward<float, 128>(a, q, st, log);
+  return a.d == 64 ? backward<bf16, 64>(a, q, st, log) : backward<bf16, 128>(a, q, st, log);
 }
 
 }  // namespace avq

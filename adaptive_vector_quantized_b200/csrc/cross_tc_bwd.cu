@@ -261,16 +261,14 @@ __device__ __forceinline__ RowTile row_tile(const CrossArgs& a, const KeyItem& x
   return RowTile{x.kb * a.per_b + rg / a.per_h, x.kh * a.per_h + rg % a.per_h, (i - rg * rtiles) * 128};
 }
 
+// The work of a block that is number `block` of `blocks`.
 template <int D, bool kWithQ>
-__global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_constant__ Maps maps,
-                                                                  const CrossArgs a, unsigned int* err, int items,
-                                                                  int ktiles, int rtiles) {
+__device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const CrossArgs& a, unsigned int* err,
+                                         int items, int ktiles, int rtiles, int block, int blocks) {
   using S = Smem<D>;
-  extern __shared__ __align__(1024) uint8_t sm[];
-  if (tc::smem_u32(sm) & 1023u) {  // no room is left to align it here
-    if (threadIdx.x == 0) atomicOr(err, kErrInternal);
-    return;
-  }
+  // kWithQ: the whole grid, by its special registers (two registers that would spill)
+  auto first = [&] { return kWithQ ? (int)blockIdx.x : block; };
+  auto stride = [&] { return kWithQ ? (int)gridDim.x : blocks; };
   const Bars bar = bars_of<D>(sm);
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
@@ -287,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  grid_dependency_wait();  // delta
-  allow_dependents();      // dQ's blocks may take the SMs that these leave
+  grid_dependency_wait();  // delta, and everything before it
+  if (kWithQ) allow_dependents();
   const Guard guard{err, sAbort};
   const uint32_t tmem = *sTmem;
   // S | dP | dV | dK, and behind them dQ of even and of odd steps
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         Turn<S::kSlotsB> tb;
         uint32_t na = 0, nb = 0, own = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        for (int i = first(); i < items && ok; i += stride()) {
           const KeyItem x = key_item(a, i, ktiles, rtiles);
           if (x.i0 >= x.i1) continue;
           ok = guard.wait(bar.own_empty, (own & 1) ^ 1);
@@ -336,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
     } else if (warp == kHelpWarp) {
       uint32_t n = 0, own = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = first(); i < items && ok; i += stride()) {
         const KeyItem x = key_item(a, i, ktiles, rtiles);
         if (kWithQ && x.i0 < x.i1) {
           // K's rows of keys that are left out become zeros: K is a factor of dS K
@@ -405,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
         }
         return true;
       };
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = first(); i < items && ok; i += stride()) {
         const KeyItem x = key_item(a, i, ktiles, rtiles);
         const int tiles = uniform(x.i1 - x.i0);
         if (tiles <= 0) continue;
@@ -491,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
       }
       return true;
     };
-    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+    for (int i = first(); i < items && ok; i += stride()) {
       const KeyItem x = key_item(a, i, ktiles, rtiles);
       if (kWithQ && x.count == 0) {  // no key: dQ = 0
         const KeyItem y = key_item(a, i, ktiles, rtiles, true);
@@ -506,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dkv_kernel(const __grid_
           }
         }
       }
-      factor = ds_scale(a, x.kb, x.count);
+      factor = lone_key(a, x.kb, x.count) ? 0.f : a.scale;
       const int key = x.k0 + quarter * 32 + lane;
       const bool live = key_seen(a, x.kb, key, x.count);
       for (int j = x.i0; j < x.i1; ++j, ++steps) {
@@ -656,18 +654,10 @@ __device__ __forceinline__ RowItem row_item(const CrossArgs& a, int i, int rtile
   return x;
 }
 
-// Starts beside the kernel of dK and dV, on the SMs that it leaves.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_constant__ Maps maps,
-                                                                 const CrossArgs a, unsigned int* err, int items,
-                                                                 int rtiles) {
+__device__ __forceinline__ void form_dq(uint8_t* sm, const Maps& maps, const CrossArgs& a, unsigned int* err,
+                                        int items, int rtiles, int block, int blocks) {
   using S = Smem<D>;
-  extern __shared__ __align__(1024) uint8_t sm[];
-  if (tc::smem_u32(sm) & 1023u) {  // no room is left to align it here
-    if (threadIdx.x == 0) atomicOr(err, kErrInternal);
-    grid_dependency_wait();
-    return;
-  }
   const Bars bar = bars_of<D>(sm);
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + S::kMisc);
   int* sAbort = reinterpret_cast<int*>(sm + S::kMisc + 4);
@@ -683,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  grid_dependency_wait();  // delta, and everything before it
   const Guard guard{err, sAbort};
   const uint32_t tmem = *sTmem;
   const uint32_t tP = tmem + 256, tQ = tmem + 384;  // S of even steps | S of odd steps | dP | dQ
@@ -695,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         Turn<S::kSlotsB> tb;
         uint32_t na = 0, nb = 0, own = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+        for (int i = block; i < items && ok; i += blocks) {
           const RowItem x = row_item(a, i, rtiles);
           if (x.t0 >= x.t1) continue;
           ok = guard.wait(bar.own_empty, (own & 1) ^ 1);
@@ -729,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
       // K's rows of keys that are left out become zeros: K is a factor of dS K too
       Turn<S::kSlotsA> ta;
       bool ok = true;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = block; i < items && ok; i += blocks) {
         const RowItem x = row_item(a, i, rtiles);
         for (int j = x.t0; j < x.t1; ++j, ta.step()) {
           ok = guard.wait(bar.a_full + ta.slot, ta.phase);
@@ -761,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         tb.step();
         return true;
       };
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = block; i < items && ok; i += blocks) {
         const RowItem x = row_item(a, i, rtiles);
         const int tiles = uniform(x.t1 - x.t0);
         if (tiles <= 0) continue;
@@ -815,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
     const float2 c2 = fm::f2(c2f, c2f);
     uint32_t steps = 0, dones = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+    for (int i = block; i < items && ok; i += blocks) {
       const RowItem x = row_item(a, i, rtiles);
       const int row = x.row0 + quarter * 32 + lane;
       const size_t at = ((size_t)x.b * a.Hq + x.h) * a.Nq + row;
@@ -880,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
         tc::tc_fence_after();
       }
       // 64 columns of dQ to a group
-      const float factor = ds_scale(a, x.kb, x.count);
+      const float factor = lone_key(a, x.kb, x.count) ? 0.f : a.scale;
       if (half < S::kBlocks) {
         if (x.parts > 1) {
           float* dst = a.part + ((size_t)(i - a.whole) * 128 + quarter * 32 + lane) * D + half * 64;
@@ -890,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
             for (int c = 0; c < 64; c += 4) *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
           }
         } else if (any) {
-          store_block(tQ + lane_off + half * 64, factor, true, out, &maps.out0, half * 64, x.row0 + quarter * 32, a.Nq,
+          store_block(tQ + lane_off + half * 64, factor, true, out, &maps.out2, half * 64, x.row0 + quarter * 32, a.Nq,
                       a.Hq > 1 ? x.h : 0, a.B > 1 ? x.b : 0, lane);
         } else if (in) {
           bf16* dst = static_cast<bf16*>(a.dQ) + at * D + half * 64;
@@ -912,7 +903,47 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_dq_kernel(const __grid_c
   tc::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
-  grid_dependency_wait();  // whatever comes after this kernel comes after dK's and dV's too
+}
+
+// ---- the launches ------------------------------------------------------------------------
+
+// Whether the shared memory is aligned; no room is left to align it in the kernel.
+__device__ __forceinline__ bool smem_aligned(const uint8_t* sm, unsigned int* err) {
+  if (!(tc::smem_u32(sm) & 1023u)) return true;
+  if (threadIdx.x == 0) atomicOr(err, kErrInternal);
+  grid_dependency_wait();
+  return false;
+}
+
+// The first key_blocks blocks form dK and dV, the others dQ with the arguments q, on the
+// SMs that those leave.  One launch for both: a kernel of its own for dQ that
+// started beside the other would read delta before its own wait for the work before
+// it, and nothing else makes another kernel's writes visible.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cross_tc_backward_kernel(const __grid_constant__ Maps maps,
+                                                                       const __grid_constant__ CrossArgs a,
+                                                                       const __grid_constant__ CrossArgs q,
+                                                                       unsigned int* err, int key_items,
+                                                                       int row_items, int ktiles, int rtiles,
+                                                                       int key_blocks) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (!smem_aligned(sm, err)) return;
+  const int block = blockIdx.x;
+  if (block < key_blocks)
+    form_dkv<D, false>(sm, maps, a, err, key_items, ktiles, rtiles, block, key_blocks);
+  else
+    form_dq<D>(sm, maps, q, err, row_items, rtiles, block - key_blocks, (int)gridDim.x - key_blocks);
+}
+
+// One key tile: all three gradients.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cross_tc_dqkv_kernel(const __grid_constant__ Maps maps,
+                                                                   const __grid_constant__ CrossArgs a,
+                                                                   unsigned int* err, int items, int ktiles,
+                                                                   int rtiles) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (!smem_aligned(sm, err)) return;
+  form_dkv<D, true>(sm, maps, a, err, items, ktiles, rtiles, blockIdx.x, gridDim.x);
 }
 
 Strides dense(int B, int H, int N, int d) {
@@ -928,46 +959,37 @@ cudaError_t maps_of(const CrossArgs& a, Maps* m) {
   return e;
 }
 
-// a, q: the arguments of the kernel of dK and dV, and of dQ's.  Each tensor map
-// takes the host most of a microsecond: the inputs' serve both kernels.
+// a, q: the arguments for dK and dV, and for dQ.
 template <int D>
 cudaError_t run(const CrossArgs& a, const CrossArgs& q, unsigned int* err, cudaStream_t st, LaunchLog& log) {
   Maps m;
-  const bool with_q = cross_tc_dkv_forms_dq(a.Nk, D);
   const Strides ks = dense(a.Bk, a.Hk, a.Nk, D), qs = dense(a.B, a.Hq, a.Nq, D);
-  CUtensorMap dq;
   cudaError_t e = maps_of<D>(a, &m);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out0, a.dV, ks, a.Bk, a.Hk, a.Nk, D, 32);
   if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out1, a.dK, ks, a.Bk, a.Hk, a.Nk, D, 32);
-  if (e == cudaSuccess) e = make_tmap_view_bf16(&dq, a.dQ, qs, a.B, a.Hq, a.Nq, D, 32);
+  if (e == cudaSuccess) e = make_tmap_view_bf16(&m.out2, a.dQ, qs, a.B, a.Hq, a.Nq, D, 32);
   if (e != cudaSuccess) return e;
-  m.out2 = dq;
   constexpr int smem = Smem<D>::kTotal;
   const int ktiles = (a.Nk + 127) / 128, rtiles = (a.Nq + 127) / 128;
   const int key_items = a.Bk * a.Hk * ktiles * a.splits;
-  const dim3 key_grid(key_items < num_sms() ? key_items : num_sms());
-  log.add(with_q ? "cross_tc_dqkv" : "cross_tc_dkv");
+  const int key_blocks = key_items < num_sms() ? key_items : num_sms();
   if constexpr (D == 64) {
-    if (with_q) {
-      e = allow_smem<cross_tc_dkv_kernel<D, true>>(smem);
+    if (cross_tc_dkv_forms_dq(a.Nk, D)) {
+      log.add("cross_tc_dqkv");
+      e = allow_smem<cross_tc_dqkv_kernel<D>>(smem);
       if (e != cudaSuccess) return e;
-      return launch_after(cross_tc_dkv_kernel<D, true>, key_grid, dim3(kThreads), smem, st, m, a, err, key_items,
+      return launch_after(cross_tc_dqkv_kernel<D>, dim3(key_blocks), dim3(kThreads), smem, st, m, a, err, key_items,
                           ktiles, rtiles);
     }
   }
-  e = allow_smem<cross_tc_dkv_kernel<D, false>>(smem);
-  if (e == cudaSuccess) e = allow_smem<cross_tc_dq_kernel<D>>(smem);
-  if (e == cudaSuccess)
-    e = launch_after(cross_tc_dkv_kernel<D, false>, key_grid, dim3(kThreads), smem, st, m, a, err, key_items, ktiles,
-                     rtiles);
+  log.add("cross_tc_backward");
+  e = allow_smem<cross_tc_backward_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
-  m.out0 = dq;
   const int items = a.B * a.Hq * rtiles;
-  const int launch = q.whole + (items - q.whole) * q.splits;
-  const dim3 grid(launch < num_sms() ? launch : num_sms());
-  log.add("cross_tc_dq");
-  // dK and dV's kernel waited for delta and writes nothing that is read here
-  e = launch_after(cross_tc_dq_kernel<D>, grid, dim3(kThreads), smem, st, m, q, err, launch, rtiles);
+  const int row_items = q.whole + (items - q.whole) * q.splits;
+  const int row_blocks = row_items < num_sms() ? row_items : num_sms();
+  e = launch_after(cross_tc_backward_kernel<D>, dim3(key_blocks + row_blocks), dim3(kThreads), smem, st, m, a, q, err,
+                   key_items, row_items, ktiles, rtiles, key_blocks);
   if (e == cudaSuccess && q.whole < items) e = launch_cross_join_items(q, items, rtiles, 128, false, st, log);
   return e;
 }

@@ -282,10 +282,10 @@ CrossPlan plan_cross(const avq_cross_dims& s, avq_dtype dt, bool backward) {
   if (p.tc) {
     const long long kb = (long long)s.Bk * s.Hk * key_tiles, qb = (long long)s.B * s.Hq * ((s.Nq + 127) / 128);
     const long long sms = num_sms();
-    // Where the items of both kernels fit the SMs, neither is cut into more than leave
+    // Where the items of both halves fit the SMs, neither is cut into more than leave
     // the other its place, and they run side by side: 300 rows and keys, 24 heads of
-    // 128: 20.8 us, 32.5 with both over all SMs, one after the other; 1024 rows and
-    // keys, 8 heads of 64: 22.5 and 33.6.
+    // 128: 19.5 us, 32.5 with both over all SMs, one after the other; 1024 rows and
+    // keys, 8 heads of 64: 23.5 and 33.6.  dK and dV have 4 of the 7 products.
     const bool beside = kb + qb <= sms && !cross_tc_dkv_forms_dq(s.Nk, s.d);
     p.dkv_splits = split_count(kb, shared * ((s.Nq + 127) / 128), beside ? sms * 4 / 7 : sms);
     p.rounds = rounds_of(qb, key_tiles, beside ? sms - kb * p.dkv_splits : sms);
@@ -532,8 +532,7 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   if (p.tc) {
     if (e == cudaSuccess) e = launch_cross_tc_backward(a, q, err, cs, log);
   } else {
-    if (e == cudaSuccess && s.Nk > 0) e = launch_cross_simt_dkv(a, dtype, cs, log);
-    if (e == cudaSuccess) e = launch_cross_simt_dq(q, dtype, cs, log);
+    if (e == cudaSuccess) e = launch_cross_simt_backward(a, q, dtype, cs, log);
     if (e == cudaSuccess && p.dq_splits > 1) e = launch_partial_sum(dtype, q.part, p.dq_splits, &dQ, 1, qn, cs, log);
   }
   if (e == cudaSuccess && s.Nk > 0 && p.dkv_splits > 1) {

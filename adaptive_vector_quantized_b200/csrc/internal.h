@@ -153,8 +153,9 @@ struct CrossArgs {
 };
 cudaError_t launch_cross_few_f32(const CrossArgs& a, cudaStream_t st, LaunchLog& log);
 cudaError_t launch_cross_simt(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
-cudaError_t launch_cross_simt_dkv(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
-cudaError_t launch_cross_simt_dq(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
+// dK and dV with a, dQ with q.
+cudaError_t launch_cross_simt_backward(const CrossArgs& a, const CrossArgs& q, avq_dtype dt, cudaStream_t st,
+                                       LaunchLog& log);
 // Joins the forward pass's partial results (softmaxes over disjoint keys).
 cudaError_t launch_cross_join(const CrossArgs& a, avq_dtype dt, cudaStream_t st, LaunchLog& log);
 // Joins the split items of the tensor-core kernels that own rows: a.splits
