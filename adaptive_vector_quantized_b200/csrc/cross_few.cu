@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
       const int kslot = n % S::kSlots, vslot = (n + 1) % S::kSlots;
       const uint8_t* kt = sm + kslot * S::kBytes;
       const uint8_t* vt = sm + vslot * S::kBytes;
-      if (!guard.wait(full + kslot, n / S::kSlots & 1)) return;
+      if (!wait_warp(guard, full + kslot, n / S::kSlots & 1)) return;
       float s[2][4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(empty + kslot);
-      if (!guard.wait(full + vslot, (n + 1) / S::kSlots & 1)) return;
+      if (!wait_warp(guard, full + vslot, (n + 1) / S::kSlots & 1)) return;
       uint4 v[4][D / 64];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
       }
     }
     // the warps' results: O over one scale of the block, then the sums
-    if (done > 0 && !guard.wait(taken, (done - 1) & 1)) return;  // the last item's have been read
+    if (done > 0 && !wait_warp(guard, taken, (done - 1) & 1)) return;  // the last item's have been read
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       z[i] += __shfl_xor_sync(0xffffffffu, z[i], 1);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(written);
-    if (!guard.wait(written, done & 1)) return;
+    if (!wait_warp(guard, written, done & 1)) return;
     for (int e = threadIdx.x; e < ROWS * (D / 4); e += kWarps * 32) {
       const int i = e / (D / 4), c = (e % (D / 4)) * 4;
       const int r = x.chunk * ROWS + i;

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       uint32_t g = 0;
       auto pass = [&](const Item* x, int j) {  // the unit with V of tile j of item x (none if null)
         const uint32_t slot = g % S::kUnits;
-        if (!guard.wait(full + slot, g / S::kUnits & 1)) return false;
+        if (!wait_warp(guard, full + slot, g / S::kUnits & 1)) return false;
         ++g;
         if (x != nullptr && !tile_full(a, j * kKeyTile, x->count))
           clear_rows<D>(sm + S::kRing + slot * S::kUnitBytes, key_bits(a, x->kb, j * kKeyTile, x->count, lane),
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
             bits[c] = __ballot_sync(0xffffffffu, key_seen(a, x.kb, k0 + 32 * c + lane, x.count));
         }
         const uint32_t sS = tS(t, half) + lane_off;
-        ok = guard.wait(s_full + 2 * t + half, s_phase >> half & 1);
+        ok = wait_warp(guard, s_full + 2 * t + half, s_phase >> half & 1);
         if (!ok) break;
         s_phase ^= 1u << half;
         tc::tc_fence_after();
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           if (__any_sync(0xffffffffu, grown)) {
             // P V of the step before must have been added.  It is ahead of the next
             // step's S in the pipe, and of `tail` when this step is the item's last.
-            if (k0 + kStep < end) ok = guard.wait(s_full + 2 * t + (half ^ 1), s_phase >> (half ^ 1) & 1);
-            else ok = guard.wait(tail + t, tail_phase);
+            if (k0 + kStep < end) ok = wait_warp(guard, s_full + 2 * t + (half ^ 1), s_phase >> (half ^ 1) & 1);
+            else ok = wait_warp(guard, tail + t, tail_phase);
             if (!ok) break;
             tc::tc_fence_after();
             const float keep = grown ? exp2f((m - step_top) * c2f) : 1.f;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       const float lse = z == 0.f ? -INFINITY : a.scale * m + logf(z);
       const bool any = x.t0 < x.t1;
       if (any) {
-        ok = guard.wait(o_full + t, o_phase);
+        ok = wait_warp(guard, o_full + t, o_phase);
         if (!ok) break;
         o_phase ^= 1;
         tc::tc_fence_after();

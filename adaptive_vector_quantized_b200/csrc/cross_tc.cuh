@@ -10,6 +10,8 @@ namespace avq {
 constexpr int kRowTile = 128;  // rows of Q in one MMA tile
 constexpr int kKeyTile = 128;  // keys of a tile
 
+constexpr uint64_t kWaitNs = 2000000000ull;
+
 // Waits end after 2 s, or soon after another warp has given up: the flag in
 // shared memory makes every role of the block leave its loop.
 struct Guard {
@@ -20,7 +22,7 @@ struct Guard {
     const uint64_t t0 = tc::globaltimer_ns();
     while (!tc::mbar_try_wait_sleep(bar, parity, 20000u)) {
       if (*abort) return false;
-      if (tc::globaltimer_ns() - t0 > 2000000000ull) {
+      if (tc::globaltimer_ns() - t0 > kWaitNs) {
         atomicOr(err, kErrTimeout);
         *abort = 1;
         return false;
@@ -30,10 +32,28 @@ struct Guard {
   }
 };
 
-// The same for a warp as a whole: all its lanes agree, so that the compiler can
-// keep what follows in uniform registers.
+// The same for a warp as a whole: all its lanes agree, so that none stays behind in an
+// operation that names all 32 when a wait runs out, and the compiler can keep what
+// follows in uniform registers.  Guard::wait alone is for lanes that work alone.
 __device__ __forceinline__ bool wait_all(const Guard& g, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, g.wait(bar, parity));
+}
+// wait_all with the lanes' agreement on every look at the barrier: for the warps that
+// work on the forward pass's rows (16384 x 16384, 8 heads of 128: 906 us, 921 with
+// wait_all; in the gradients wait_all: 8192 x 4096, 8 heads of 128 on 4: 406, 419 with
+// this).
+__device__ __forceinline__ bool wait_warp(const Guard& g, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = tc::globaltimer_ns();
+  while (!__all_sync(0xffffffffu, tc::mbar_try_wait_sleep(bar, parity, 20000u))) {
+    const bool late = tc::globaltimer_ns() - t0 > kWaitNs;
+    if (late) {
+      atomicOr(g.err, kErrTimeout);
+      *g.abort = 1;
+    }
+    if (__any_sync(0xffffffffu, late || *g.abort)) return false;
+  }
+  return true;
 }
 // A value that every lane holds, known to the compiler as such.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }

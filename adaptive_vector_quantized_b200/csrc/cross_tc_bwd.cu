@@ -338,7 +338,7 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
         const KeyItem x = key_item(a, i, ktiles, rtiles);
         if (kWithQ && x.i0 < x.i1) {
           // K's rows of keys that are left out become zeros: K is a factor of dS K
-          ok = guard.wait(bar.own_full, own & 1);
+          ok = wait_all(guard, bar.own_full, own & 1);
           if (!ok) break;
           ++own;
           if (!tile_full(a, x.k0, x.count))
@@ -356,7 +356,7 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
             l[e] = in ? row_shift(__ldg(a.lse + head + row)) : -INFINITY;
             d[e] = in ? -__ldg(a.delta + head + row) : 0.f;
           }
-          ok = guard.wait(bar.rows_empty + (n & 1), (n >> 1 & 1) ^ 1);
+          ok = wait_all(guard, bar.rows_empty + (n & 1), (n >> 1 & 1) ^ 1);
           if (!ok) break;
           float* dst = sRows + (n & 1) * 256;
 #pragma unroll
@@ -478,7 +478,7 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
     // dQ of step n: its group (they take turns) writes the rows
     auto write_q = [&](uint32_t n) {
       const uint32_t buf = n & 1;
-      if (!guard.wait(bar.dq_full + buf, n >> 1 & 1)) return false;
+      if (!wait_all(guard, bar.dq_full + buf, n >> 1 & 1)) return false;
       tc::tc_fence_after();
       if (half == (int)buf) {
         store_block(tQ + buf * D + lane_off, factor, true, sm + S::kOutQ + warp * 4096, &maps.out2, 0,
@@ -509,7 +509,7 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
       const bool live = key_seen(a, x.kb, key, x.count);
       for (int j = x.i0; j < x.i1; ++j, ++steps) {
         const float* rows = sRows + (steps & 1) * 256 + half * 64;
-        ok = guard.wait(bar.rows_full + (steps & 1), steps >> 1 & 1) && guard.wait(bar.s_full + half, steps & 1);
+        ok = wait_all(guard, bar.rows_full + (steps & 1), steps >> 1 & 1) && wait_all(guard, bar.s_full + half, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
         float2 p[32];
@@ -536,7 +536,7 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar.p_ready + half);
-        ok = guard.wait(bar.dp_full + half, steps & 1);
+        ok = wait_all(guard, bar.dp_full + half, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
         tc::tmem_ld32(tP + lane_off + half * 64, r);
@@ -594,7 +594,7 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
       const size_t elems = (size_t)a.Bk * a.Hk * a.Nk * D;
       const size_t at = (((size_t)x.kb * a.Hk + x.kh) * a.Nk + key) * D;
       if (any) {
-        ok = guard.wait(bar.done, dones & 1);
+        ok = wait_all(guard, bar.done, dones & 1);
         if (!ok) break;
         ++dones;
         tc::tc_fence_after();
@@ -723,7 +723,7 @@ __device__ __forceinline__ void form_dq(uint8_t* sm, const Maps& maps, const Cro
       for (int i = block; i < items && ok; i += blocks) {
         const RowItem x = row_item(a, i, rtiles);
         for (int j = x.t0; j < x.t1; ++j, ta.step()) {
-          ok = guard.wait(bar.a_full + ta.slot, ta.phase);
+          ok = wait_all(guard, bar.a_full + ta.slot, ta.phase);
           if (!ok) break;
           if (!tile_full(a, j * 128, x.count))  // rows past the tensor's end came as zeros
             clear_rows<D>(sm + S::kRingA + ta.slot * S::kTileBytes, key_bits(a, x.kb, j * 128, x.count, lane),
@@ -822,7 +822,7 @@ __device__ __forceinline__ void form_dq(uint8_t* sm, const Maps& maps, const Cro
           for (int w = 0; w < 2; ++w)
             bits[w] = __ballot_sync(0xffffffffu, key_seen(a, x.kb, j * 128 + half * 64 + 32 * w + lane, x.count));
         }
-        ok = guard.wait(bar.s_full + (steps & 1), steps >> 1 & 1);
+        ok = wait_all(guard, bar.s_full + (steps & 1), steps >> 1 & 1);
         if (!ok) break;
         tc::tc_fence_after();
         float2 p[32];
@@ -835,7 +835,7 @@ __device__ __forceinline__ void form_dq(uint8_t* sm, const Maps& maps, const Cro
         if (lane == 0) tc::mbar_arrive(bar.p_ready + (steps & 1));  // S is in registers
 #pragma unroll
         for (int c = 0; c < 2; ++c) exp_chunk<false>(r + c * 32, c2, nullptr, nl, p + c * 16);
-        ok = guard.wait(bar.dp_full, steps & 1);
+        ok = wait_all(guard, bar.dp_full, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
         tc::tmem_ld32(tP + lane_off + half * 64, r);
@@ -865,7 +865,7 @@ __device__ __forceinline__ void form_dq(uint8_t* sm, const Maps& maps, const Cro
       if (!ok) break;
       const bool any = x.t0 < x.t1;
       if (any) {
-        ok = guard.wait(bar.done, dones & 1);
+        ok = wait_all(guard, bar.done, dones & 1);
         if (!ok) break;
         ++dones;
         tc::tc_fence_after();

@@ -57,3 +57,17 @@ def test_kernels_read_nothing_before_their_wait(name):
             first = reads.search(one)
             end = first.start() if first else len(one)
             assert always_at(one, "grid_dependency_wait()") < end, (kernel, part, first and first.group())
+
+
+@pytest.mark.parametrize("name", ["cross_few.cu", "cross_tc.cu", "cross_tc_bwd.cu"])
+def test_warps_wait_as_a_whole(name):
+    """Where a wait runs out, lanes that each decide for themselves could part before an operation that names all
+    32: a wait by lanes stands only where one lane works alone."""
+    text = source(name)
+    alone = []
+    for m in re.finditer(r"if \(lane == 0\) \{", text):
+        alone.append((m.start(), block(text, m.start())[1]))
+    waits = [m.start() for m in re.finditer(r"guard\.wait\(", text)]
+    assert waits and re.search(r"wait_(all|warp)\(guard", text)
+    for w in waits:
+        assert any(a < w < b for a, b in alone), text[w - 80:w + 60]
