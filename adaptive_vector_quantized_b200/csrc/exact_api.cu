@@ -58,9 +58,26 @@ avq_status view(const avq_strides* s, int B, int H, int N, int d, avq_dtype dt, 
   return AVQ_OK;
 }
 
-bool overlap(const void* x, size_t xn, const void* y, size_t yn) {
-  const char *a = static_cast<const char*>(x), *b = static_cast<const char*>(y);
-  return a < b + yn && b < a + xn;
+// Memory that a call reads or writes; of 0 bytes where it does not.
+struct Range {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+// Every output apart from every input and every other output.
+template <size_t kOuts, size_t kIns>
+avq_status apart(const Range (&outs)[kOuts], const Range (&ins)[kIns]) {
+  auto meet = [](const Range& x, const Range& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p != nullptr && y.p != nullptr && x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes;
+  };
+  for (size_t o = 0; o < kOuts; ++o) {
+    for (const Range& in : ins)
+      if (meet(outs[o], in)) return api_fail(AVQ_ERR_INVALID_ARG, "%s overlaps %s", outs[o].name, in.name);
+    for (size_t i = 0; i < o; ++i)
+      if (meet(outs[o], outs[i])) return api_fail(AVQ_ERR_INVALID_ARG, "%s overlaps %s", outs[o].name, outs[i].name);
+  }
+  return AVQ_OK;
 }
 
 avq_status check_ws(size_t need, const void* ws, size_t bytes) {
@@ -131,9 +148,7 @@ avq_status pair_of(const avq_qk_dims& s, avq_dtype dt, const void* q, const avq_
   }
   return AVQ_OK;
 }
-// Dense outputs, apart from each other and from the inputs.
-avq_status outputs_of(const avq_qk_dims& s, avq_dtype dt, void* q, const char* qn, void* k, const char* kn,
-                      const Pair* ins, int count, void** out) {
+avq_status outputs_of(const avq_qk_dims& s, void* q, const char* qn, void* k, const char* kn, void** out) {
   AVQ_TRY(need_ptr(q, qn));
   out[0] = q;
   out[1] = nullptr;
@@ -141,16 +156,19 @@ avq_status outputs_of(const avq_qk_dims& s, avq_dtype dt, void* q, const char* q
     AVQ_TRY(need_ptr(k, kn));
     out[1] = k;
   }
-  const size_t bytes[2] = {(size_t)s.B * s.Hq * s.N * s.d * elem(dt), (size_t)s.B * s.Hk * s.N * s.d * elem(dt)};
-  const char* names[2] = {qn, kn};
-  for (int o = 0; o < (s.Hk > 0 ? 2 : 1); ++o)
-    for (int i = 0; i < count; ++i)
-      for (int w = 0; w < (s.Hk > 0 ? 2 : 1); ++w)
-        if (overlap(out[o], bytes[o], ins[i].x[w], ins[i].span[w]))
-          return api_fail(AVQ_ERR_INVALID_ARG, "%s overlaps an input", names[o]);
-  if (s.Hk > 0 && overlap(q, bytes[0], k, bytes[1])) return api_fail(AVQ_ERR_INVALID_ARG, "%s and %s overlap", qn, kn);
   return AVQ_OK;
 }
+// The memory of dense outputs, of a vector [d], of positions and frequencies.
+Range dense_of(const avq_qk_dims& s, avq_dtype dt, const void* p, int H, const char* name) {
+  return Range{p, (size_t)s.B * H * s.N * s.d * elem(dt), name};
+}
+Range vector_of(const avq_qk_dims& s, size_t size, const void* p, const char* name) {
+  return Range{p, (size_t)s.d * size, name};
+}
+Range positions_of(const avq_qk_dims& s, const int32_t* p) {
+  return Range{p, s.rot > 0 ? (size_t)(s.pos_batch ? s.B : 1) * s.N * s.axes * sizeof(int32_t) : 0, "positions"};
+}
+Range freqs_of(const avq_qk_dims& s, const double* p) { return Range{p, (size_t)s.rot / 2 * sizeof(double), "freqs"}; }
 
 // ---- attention over another sequence -------------------------------------------
 
@@ -324,6 +342,9 @@ avq_status cross_inputs(const avq_cross_dims& s, avq_dtype dt, const void* Q, co
   return AVQ_OK;
 }
 
+Range lens_of(const avq_cross_dims& s, const int32_t* p) { return Range{p, (size_t)s.Bk * sizeof(int32_t), "kv_lens"}; }
+Range mask_of(const avq_cross_dims& s, const uint8_t* p) { return Range{p, (size_t)s.Bk * s.Nk, "key_mask"}; }
+
 }  // namespace
 }  // namespace avq
 
@@ -341,7 +362,10 @@ avq_status avq_rotary(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, c
   Pair in;
   void* out[2];
   AVQ_TRY(pair_of(*dims, dtype, Q, q_strides, "Q", K, k_strides, "K", &in));
-  AVQ_TRY(outputs_of(*dims, dtype, Yq, "Yq", Yk, "Yk", &in, 1, out));
+  AVQ_TRY(outputs_of(*dims, Yq, "Yq", Yk, "Yk", out));
+  AVQ_TRY(apart({dense_of(*dims, dtype, out[0], dims->Hq, "Yq"), dense_of(*dims, dtype, out[1], dims->Hk, "Yk")},
+                {{in.x[0], in.span[0], "Q"}, {in.x[1], in.span[1], "K"}, positions_of(*dims, positions),
+                 freqs_of(*dims, freqs)}));
   if (api_injected("rotary")) return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_rotary)");
   const void* none[2] = {nullptr, nullptr};
   LaunchLog log{};
@@ -365,7 +389,12 @@ avq_status avq_qk_norm(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, 
   AVQ_TRY(optional_vector(wk, "wk"));
   AVQ_TRY(optional_vector(bq, "bq"));
   AVQ_TRY(optional_vector(bk, "bk"));
-  AVQ_TRY(outputs_of(*dims, dtype, Yq, "Yq", Yk, "Yk", &in, 1, out));
+  AVQ_TRY(outputs_of(*dims, Yq, "Yq", Yk, "Yk", out));
+  const size_t es = elem(dtype);
+  AVQ_TRY(apart({dense_of(*dims, dtype, out[0], dims->Hq, "Yq"), dense_of(*dims, dtype, out[1], dims->Hk, "Yk")},
+                {{in.x[0], in.span[0], "Q"}, {in.x[1], in.span[1], "K"}, vector_of(*dims, es, wq, "wq"),
+                 vector_of(*dims, es, wk, "wk"), vector_of(*dims, es, bq, "bq"), vector_of(*dims, es, bk, "bk"),
+                 positions_of(*dims, positions), freqs_of(*dims, freqs)}));
   if (api_injected("qk_norm")) return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_qk_norm)");
   const void* w[2] = {wq, wk};
   const void* b[2] = {bq, bk};
@@ -398,17 +427,24 @@ avq_status avq_qk_norm_backward(const avq_qk_dims* dims, avq_dtype dtype, const 
   AVQ_TRY(pair_of(*dims, dtype, Q, q_strides, "Q", K, k_strides, "K", &in[1]));
   AVQ_TRY(optional_vector(wq, "wq"));
   AVQ_TRY(optional_vector(wk, "wk"));
-  AVQ_TRY(outputs_of(*dims, dtype, dQ, "dQ", dK, "dK", in, 2, out));
-  AVQ_TRY(optional_vector(dwq, "dwq"));
-  AVQ_TRY(optional_vector(dwk, "dwk"));
-  AVQ_TRY(optional_vector(dbq, "dbq"));
-  AVQ_TRY(optional_vector(dbk, "dbk"));
-  AVQ_TRY(check_ws(up256(qk_norm_backward_workspace(*dims)), ws, ws_bytes));
+  AVQ_TRY(outputs_of(*dims, dQ, "dQ", dK, "dK", out));
+  float* dw[2] = {dwq, dims->Hk > 0 ? dwk : nullptr};  // without keys theirs are ignored
+  float* db[2] = {dbq, dims->Hk > 0 ? dbk : nullptr};
+  AVQ_TRY(optional_vector(dw[0], "dwq"));
+  AVQ_TRY(optional_vector(dw[1], "dwk"));
+  AVQ_TRY(optional_vector(db[0], "dbq"));
+  AVQ_TRY(optional_vector(db[1], "dbk"));
+  const size_t es = elem(dtype), need = up256(qk_norm_backward_workspace(*dims));
+  AVQ_TRY(check_ws(need, ws, ws_bytes));
+  AVQ_TRY(apart({dense_of(*dims, dtype, out[0], dims->Hq, "dQ"), dense_of(*dims, dtype, out[1], dims->Hk, "dK"),
+                 vector_of(*dims, 4, dw[0], "dwq"), vector_of(*dims, 4, dw[1], "dwk"), vector_of(*dims, 4, db[0], "dbq"),
+                 vector_of(*dims, 4, db[1], "dbk"), {ws, need, "the workspace"}},
+                {{in[0].x[0], in[0].span[0], "dYq"}, {in[0].x[1], in[0].span[1], "dYk"}, {in[1].x[0], in[1].span[0], "Q"},
+                 {in[1].x[1], in[1].span[1], "K"}, vector_of(*dims, es, wq, "wq"), vector_of(*dims, es, wk, "wk"),
+                 positions_of(*dims, positions), freqs_of(*dims, freqs)}));
   if (api_injected("qk_norm_backward"))
     return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_qk_norm_backward)");
   const void* w[2] = {wq, wk};
-  float* dw[2] = {dwq, dims->Hk > 0 ? dwk : nullptr};
-  float* db[2] = {dbq, dims->Hk > 0 ? dbk : nullptr};
   LaunchLog log{};
   const cudaError_t e = launch_qk_norm_backward(*dims, dtype, in[0].x, in[0].s, in[1].x, in[1].s, w, positions, freqs,
                                                 out, dw, db, ws, reinterpret_cast<cudaStream_t>(stream), log);
@@ -434,19 +470,11 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
   AVQ_TRY(need_ptr(O, "O"));
   AVQ_TRY(view(o_strides, s.B, s.Hq, s.Nq, s.d, dtype, kWritten, "O", &a.os, &ospan));
-  const void* ins[3] = {Q, K, V};
-  for (int i = 0; i < 3; ++i)
-    if (spans[i] > 0 && overlap(O, ospan, ins[i], spans[i])) return api_fail(AVQ_ERR_INVALID_ARG, "O overlaps an input");
   AVQ_TRY(optional_vector(lse, "lse"));
-  if (lse != nullptr) {
-    const size_t n = (size_t)s.B * s.Hq * s.Nq * sizeof(float);
-    for (int i = 0; i < 3; ++i)
-      if (spans[i] > 0 && overlap(lse, n, ins[i], spans[i]))
-        return api_fail(AVQ_ERR_INVALID_ARG, "lse overlaps an input");
-    if (overlap(lse, n, O, ospan)) return api_fail(AVQ_ERR_INVALID_ARG, "lse overlaps O");
-  }
   const CrossPlan p = plan_cross(s, dtype, false);
   AVQ_TRY(check_ws(p.total(), ws, ws_bytes));
+  AVQ_TRY(apart({{O, ospan, "O"}, {lse, (size_t)s.B * s.Hq * s.Nq * sizeof(float), "lse"}, {ws, p.total(), "the workspace"}},
+                {{Q, spans[0], "Q"}, {K, spans[1], "K"}, {V, spans[2], "V"}, lens_of(s, kv_lens), mask_of(s, key_mask)}));
   if (api_path() == AVQ_PATH_TC && dtype != AVQ_BF16)
     return api_fail(AVQ_ERR_UNSUPPORTED, "no tensor-core kernel for this type");
   if (api_injected("cross_attention"))
@@ -482,7 +510,7 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
   AVQ_TRY(check_cross(dims, dtype));
   const avq_cross_dims& s = *dims;
   CrossArgs a{};
-  size_t spans[6];
+  size_t spans[5];
   AVQ_TRY(cross_inputs(s, dtype, Q, q_strides, K, k_strides, V, v_strides, kv_lens, key_mask, &a, spans));
   AVQ_TRY(need_ptr(dO, "dO"));
   AVQ_TRY(view(do_strides, s.B, s.Hq, s.Nq, s.d, dtype, kCopied, "dO", &a.gs, &spans[3]));
@@ -494,20 +522,12 @@ avq_status avq_cross_attention_backward(const avq_cross_dims* dims, avq_dtype dt
     AVQ_TRY(need_ptr(dK, "dK"));
     AVQ_TRY(need_ptr(dV, "dV"));
   }
-  const size_t qn = (size_t)s.B * s.Hq * s.Nq * s.d, kn = (size_t)s.Bk * s.Hk * s.Nk * s.d;
-  const void* ins[6] = {Q, K, V, dO, O, lse};
-  spans[5] = (size_t)s.B * s.Hq * s.Nq * sizeof(float);
-  const void* outs[3] = {dQ, dK, dV};
-  const size_t bytes[3] = {qn * elem(dtype), kn * elem(dtype), kn * elem(dtype)};
-  for (int o = 0; o < (s.Nk > 0 ? 3 : 1); ++o) {
-    for (int i = 0; i < 6; ++i)
-      if (spans[i] > 0 && overlap(outs[o], bytes[o], ins[i], spans[i]))
-        return api_fail(AVQ_ERR_INVALID_ARG, "a gradient overlaps an input");
-    for (int i = 0; i < o; ++i)
-      if (overlap(outs[o], bytes[o], outs[i], bytes[i])) return api_fail(AVQ_ERR_INVALID_ARG, "gradients overlap");
-  }
+  const size_t qn = (size_t)s.B * s.Hq * s.Nq * s.d, kn = (size_t)s.Bk * s.Hk * s.Nk * s.d, es = elem(dtype);
   const CrossPlan p = plan_cross(s, dtype, true);
   AVQ_TRY(check_ws(p.total(), ws, ws_bytes));
+  AVQ_TRY(apart({{dQ, qn * es, "dQ"}, {dK, kn * es, "dK"}, {dV, kn * es, "dV"}, {ws, p.total(), "the workspace"}},
+                {{Q, spans[0], "Q"}, {K, spans[1], "K"}, {V, spans[2], "V"}, {dO, spans[3], "dO"}, {O, spans[4], "O"},
+                 {lse, (size_t)s.B * s.Hq * s.Nq * sizeof(float), "lse"}, lens_of(s, kv_lens), mask_of(s, key_mask)}));
   if (api_path() == AVQ_PATH_TC && dtype != AVQ_BF16)
     return api_fail(AVQ_ERR_UNSUPPORTED, "no tensor-core kernel for this type");
   if (api_injected("cross_attention_backward"))

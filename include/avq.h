@@ -337,6 +337,8 @@ avq_status avq_gilbert_order(int width, int height, int32_t* idx);
  * training needs.  Inputs may be views: a tensor [B,H,N,d] is given by its
  * address and avq_strides, so that the heads of a joint projection's output
  * are read in place.  Outputs are dense unless strides are taken for them.
+ * Outputs and workspace overlap no input and not each other (a view counts from
+ * its first element to its last).
  */
 
 /* Strides, in elements, of batch entry, head and token of a [B,H,N,d] tensor
@@ -376,8 +378,8 @@ typedef struct {
  * positions of a token are then n); freqs fp64 [rot/2], as avq_rotary_freqs
  * makes them.  inverse != 0 turns the other way (mscale stays a factor): the
  * gradient of the forward call.  dims->norm must be AVQ_NORM_NONE.
- * Outputs: Yq [B,Hq,N,d], Yk [B,Hk,N,d], dense, not overlapping the inputs.
- * K, Yk and k_strides are ignored when Hk == 0.
+ * Outputs: Yq [B,Hq,N,d], Yk [B,Hk,N,d], dense.  K, Yk and k_strides (and in the
+ * calls below the keys' gradients) are ignored when Hk == 0.
  */
 avq_status avq_rotary(const avq_qk_dims* dims, avq_dtype dtype, const void* Q, const avq_strides* q_strides,
                       const void* K, const avq_strides* k_strides, const int32_t* positions,
@@ -458,8 +460,7 @@ typedef struct {
  * -inf alone, gives O = 0 and lse = -inf; one with a score of NaN or +inf
  * gives NaN.
  * Outputs (device): O [B,Hq,Nq,d] of `dtype` with strides; lse fp32
- * [B,Hq,Nq], dense, or NULL.  O and lse overlap no input and not each other;
- * O's strides let no two rows overlap.
+ * [B,Hq,Nq], dense, or NULL.  O's strides let no two rows overlap.
  * Workspace: avq_cross_workspace_size(dims, dtype, 0) bytes, 256-byte
  * aligned; NULL when that is 0.  It depends on the kernel family
  * (avq_set_path) in force, as the call does.
