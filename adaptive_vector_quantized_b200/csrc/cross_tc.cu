@@ -37,7 +37,8 @@ constexpr int kMmaWarp = kSoftmaxWarps;  // and the next: one for each tile of a
 constexpr int kLoadWarp = kMmaWarp + 2, kCleanWarp = kLoadWarp + 1;
 constexpr int kThreads = 384;  // three warpgroups
 // Registers per thread: 168 at launch (64512 in all), then 216 for the softmax
-// groups' row of 128 scores and 72 for the third (2 * 216 + 72 = 3 * 168).
+// groups, whose threads hold a row's 64 scores and as many of their results, and 72
+// for the third (2 * 216 + 72 = 3 * 168).
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 
 template <int D>

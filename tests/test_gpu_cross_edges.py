@@ -162,3 +162,20 @@ def test_keys_left_out_get_zero_whatever_the_rows_hold(Nk, d, family):
         out = t.cpu()[:, 0]
         assert (out[~keep] == 0).all()
         assert not torch.isfinite(out[keep]).all(-1).any()
+
+
+# ---- steep scores ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_over_dense_inputs_and_rising_scores(d, family):
+    """Dense tensors, and keys ordered so that a row's scores rise by 60: nearly all keys weigh next to nothing."""
+    Q, K, V, dO, _ = inputs(1, 1, 2, 2, 160, 1000, d, family, 4, packed=False)
+    Q[..., 0] = 1.0
+    K[..., 0] = torch.linspace(0.0, 60.0, 1000).to(family).cuda()
+    want = ref.cross(Q, K, V, scale=1.0)
+    O, lse = want["O"].to(family).cuda(), want["lse"].float().cuda()
+    want = ref.cross(Q, K, V, scale=1.0, dO=dO, O_given=O)
+    got = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse, scale=1.0)
+    for n, t in zip(("dQ", "dK", "dV"), got):
+        ref.check(n, t, want[n], want[n + "_tol"])
