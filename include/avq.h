@@ -371,8 +371,9 @@ typedef struct {
 /*
  * avq_rotary -- rotation of queries and keys by position.
  * Pair i of token n turns by the angle positions[n] * freqs[i]; elements past
- * rot are copied.  Angles are formed and reduced in 64 bits, so far positions
- * lose nothing.
+ * rot are copied.  Angles are formed and reduced in 64 bits: they are off by at
+ * most 2^-26 of a turn and 2^-52 of the whole angle (2^-24 of a turn at position
+ * 10^9).
  * Inputs (device): Q, K of `dtype` with strides; positions int32 [N] or
  * [B,N], with axes == 2 [N,2] or [B,N,2] (NULL: 0..N-1; with axes == 2 both
  * positions of a token are then n); freqs fp64 [rot/2], as avq_rotary_freqs
