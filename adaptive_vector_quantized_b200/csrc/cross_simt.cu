@@ -21,10 +21,9 @@
 // inputs run beside the products: V's beside Q K^T, the next K's beside P V, for dK
 // and dV the next step's rows beside this one's (in dQ V and K take one place, one
 // after the other, so that another block of the SM covers them).  24 heads of 1000
-// rows and keys of 128: 411 us (30 TFLOP/s; 463 with K and V in one place, 549 with
-// loads that nothing covers), gradients 1.39 ms.  8 x 4
-// scores a thread, with half the threads: 511 us where 4 x 4 took 463, as too few
-// warps are left to cover anything.
+// rows and keys of 128: 406 us (30 TFLOP/s; 463 with K and V in one place, 549 with
+// loads that nothing covers), gradients 1.39 ms.  8 x 4 scores a thread, with half the
+// threads: 511 us where 4 x 4 took 463, as too few warps are left to cover anything.
 #include "cross.cuh"
 #include "fastmath.cuh"
 

@@ -16,7 +16,8 @@
 // room for a second buffer at d = 128); 16384 x 16384, 8 heads of 128: 1.36 ms
 // like that, 1.03 ms in halves, although a product with 64 columns takes 48
 // clocks of shared memory reads instead of 32.  With the last round's items split
-// over the keys 0.90 ms (1.22 PFLOP/s).
+// over the keys 0.91 ms (1.21 PFLOP/s; captured, in bursts: run for seconds the power
+// cap makes it 1.05).
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the scale in use (P then stays below 2^8, and its rounding to bf16

@@ -5,7 +5,7 @@
 // order and no gradient passes through memory in fp32.
 //
 //   P = exp(S - lse),  dP = dO V^T,  dS = P (dP - delta),
-//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K  (0 for scale with one key alone).
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K;  dK = dQ = 0 with one key alone.
 //
 // A block has two groups of four warps for the elementwise work (a TMEM lane to
 // a thread, half of the tile's columns to a group), a warp that loads by TMA, one
@@ -22,15 +22,15 @@
 // with 64 columns takes 48 clocks of shared memory reads, one with 128 takes 64.
 // What bound both most was the MMA warps' own issue: run converged, with their
 // descriptors in uniform registers, they brought the whole call from 463 to 394 us
-// (875 TFLOP/s of the 5 products that the formulas need).
-#include "cross_tc.cuh"
-
+// (captured, in bursts; 407 us now, with every wait agreed on by its warp: 845 TFLOP/s
+// of the 5 products that the formulas need; 467 under the power cap, run for seconds).
 //
 // With at most one key tile (text states) and d = 64 the dK/dV blocks see every
 // key of a row, and TMEM has room: they form dQ too, from a copy of dS in shared
 // memory (the rows of dS^T are keys, so it is read column by column), and Q and
 // dO are read once: 24 heads of 4096 rows over 77 keys 65 us apart, 39 us so,
 // 32 us with the converged MMA warps.
+#include "cross_tc.cuh"
 
 namespace avq {
 
@@ -180,8 +180,8 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* r, float2 c2, const fl
 // 64 columns of an accumulator row (times f; 0 for a key that is left out, `on`
 // false, whatever the rows held), as bf16 into the warp's staging rows, then to
 // memory by TMA.
-__device__ __forceinline__ void store_block(uint32_t taddr, float f, bool on, uint8_t* out, const CUtensorMap* map, int col,
-                                            int row, int rows, int h, int b, int lane) {
+__device__ __forceinline__ void store_block(uint32_t taddr, float f, bool on, uint8_t* out, const CUtensorMap* map,
+                                            int col, int row, int rows, int h, int b, int lane) {
   if (lane == 0) tc::bulk_wait_group_read0();
   __syncwarp();
 #pragma unroll
@@ -509,7 +509,8 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
       const bool live = key_seen(a, x.kb, key, x.count);
       for (int j = x.i0; j < x.i1; ++j, ++steps) {
         const float* rows = sRows + (steps & 1) * 256 + half * 64;
-        ok = wait_all(guard, bar.rows_full + (steps & 1), steps >> 1 & 1) && wait_all(guard, bar.s_full + half, steps & 1);
+        ok = wait_all(guard, bar.rows_full + (steps & 1), steps >> 1 & 1) &&
+             wait_all(guard, bar.s_full + half, steps & 1);
         if (!ok) break;
         tc::tc_fence_after();
         float2 p[32];
@@ -609,8 +610,8 @@ __device__ __forceinline__ void form_dkv(uint8_t* sm, const Maps& maps, const Cr
       } else if (any) {
 #pragma unroll
         for (int cb = 0; cb < S::kBlocks; ++cb)
-          store_block(acc + cb * 64, f, live, out, half == 0 ? &maps.out0 : &maps.out1, cb * 64, x.k0 + quarter * 32, a.Nk,
-                      a.Hk > 1 ? x.kh : 0, a.Bk > 1 ? x.kb : 0, lane);
+          store_block(acc + cb * 64, f, live, out, half == 0 ? &maps.out0 : &maps.out1, cb * 64,
+                      x.k0 + quarter * 32, a.Nk, a.Hk > 1 ? x.kh : 0, a.Bk > 1 ? x.kb : 0, lane);
       } else if (key < a.Nk) {
         bf16* dst = static_cast<bf16*>(half == 0 ? a.dV : a.dK) + at;
         for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);

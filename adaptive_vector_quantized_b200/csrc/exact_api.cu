@@ -229,7 +229,8 @@ constexpr long long kFewRowsF32 = 24;
 // tiles, fill its rounds: the items of full rounds stay whole, those of the last
 // round are split where two or more parts of at least four tiles each fit it.
 // 64 pairs of row tiles of each of 8 heads of 128 over 16384 keys (3.46 rounds): 990
-// us whole, 909 us with the last round split in two.
+// us whole, 909 us with the last round split in two (captured, in bursts).  64 parts at
+// most, as in split_count: not measured.
 struct Rounds {
   int whole = 0, splits = 1;
   long long parts = 0;  // partial results
@@ -437,10 +438,11 @@ avq_status avq_qk_norm_backward(const avq_qk_dims* dims, avq_dtype dtype, const 
   const size_t es = elem(dtype), need = up256(qk_norm_backward_workspace(*dims));
   AVQ_TRY(check_ws(need, ws, ws_bytes));
   AVQ_TRY(apart({dense_of(*dims, dtype, out[0], dims->Hq, "dQ"), dense_of(*dims, dtype, out[1], dims->Hk, "dK"),
-                 vector_of(*dims, 4, dw[0], "dwq"), vector_of(*dims, 4, dw[1], "dwk"), vector_of(*dims, 4, db[0], "dbq"),
-                 vector_of(*dims, 4, db[1], "dbk"), {ws, need, "the workspace"}},
-                {{in[0].x[0], in[0].span[0], "dYq"}, {in[0].x[1], in[0].span[1], "dYk"}, {in[1].x[0], in[1].span[0], "Q"},
-                 {in[1].x[1], in[1].span[1], "K"}, vector_of(*dims, es, wq, "wq"), vector_of(*dims, es, wk, "wk"),
+                 vector_of(*dims, 4, dw[0], "dwq"), vector_of(*dims, 4, dw[1], "dwk"),
+                 vector_of(*dims, 4, db[0], "dbq"), vector_of(*dims, 4, db[1], "dbk"), {ws, need, "the workspace"}},
+                {{in[0].x[0], in[0].span[0], "dYq"}, {in[0].x[1], in[0].span[1], "dYk"},
+                 {in[1].x[0], in[1].span[0], "Q"}, {in[1].x[1], in[1].span[1], "K"},
+                 vector_of(*dims, es, wq, "wq"), vector_of(*dims, es, wk, "wk"),
                  positions_of(*dims, positions), freqs_of(*dims, freqs)}));
   if (api_injected("qk_norm_backward"))
     return api_fail(AVQ_ERR_CUDA, "injected failure before launch (avq_qk_norm_backward)");
@@ -473,8 +475,11 @@ avq_status avq_cross_attention(const avq_cross_dims* dims, avq_dtype dtype, cons
   AVQ_TRY(optional_vector(lse, "lse"));
   const CrossPlan p = plan_cross(s, dtype, false);
   AVQ_TRY(check_ws(p.total(), ws, ws_bytes));
-  AVQ_TRY(apart({{O, ospan, "O"}, {lse, (size_t)s.B * s.Hq * s.Nq * sizeof(float), "lse"}, {ws, p.total(), "the workspace"}},
-                {{Q, spans[0], "Q"}, {K, spans[1], "K"}, {V, spans[2], "V"}, lens_of(s, kv_lens), mask_of(s, key_mask)}));
+  AVQ_TRY(apart({{O, ospan, "O"},
+                 {lse, (size_t)s.B * s.Hq * s.Nq * sizeof(float), "lse"},
+                 {ws, p.total(), "the workspace"}},
+                {{Q, spans[0], "Q"}, {K, spans[1], "K"}, {V, spans[2], "V"}, lens_of(s, kv_lens),
+                 mask_of(s, key_mask)}));
   if (api_path() == AVQ_PATH_TC && dtype != AVQ_BF16)
     return api_fail(AVQ_ERR_UNSUPPORTED, "no tensor-core kernel for this type");
   if (api_injected("cross_attention"))
