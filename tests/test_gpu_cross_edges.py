@@ -179,3 +179,48 @@ def test_gradients_over_dense_inputs_and_rising_scores(d, family):
     got = avq.avq_cross_attention_backward(dO, Q, K, V, O, lse, scale=1.0)
     for n, t in zip(("dQ", "dK", "dV"), got):
         ref.check(n, t, want[n], want[n + "_tol"])
+
+
+@pytest.mark.parametrize("Nk, d", [(77, 64), (300, 64), (300, 128)])
+def test_masks_of_calls_in_a_row_share_a_workspace(Nk, d, family):
+    """Calls with one key and with many after one another, eager and captured, and two streams side by side."""
+    Q, K, V, dO, g = inputs(2, 2, 4, 2, 200, Nk, d, family, 37)
+    few = torch.zeros(2, Nk, dtype=torch.bool, device="cuda")
+    few[0, Nk - 1] = few[1, 5] = True
+    masks = [few, (torch.rand(2, Nk, generator=g) < 0.5).cuda(), few.flip(0).contiguous()]
+    sets = []
+    for m in masks:
+        O, lse = avq.avq_cross_attention(Q, K, V, key_mask=m, lse=True)
+        sets.append(((dO, Q, K, V, O, lse), dict(key_mask=m)))
+    want = []
+    for a, kw in sets:
+        torch.cuda.synchronize()
+        want.append(avq.avq_cross_attention_backward(*a, **kw))
+    assert (want[0][0] == 0).all() and (want[1][0] != 0).any() and (want[2][1] == 0).all()
+    dims = avq.avq_cross_dims(2, 2, 4, 2, 200, Nk, d, d ** -0.5)
+    size = avq.avq_cross_workspace_size(dims, avq.AVQ_F32 if family == torch.float32 else avq.AVQ_BF16, True)
+    ws = torch.full((size + 256,), 255, dtype=torch.uint8, device="cuda")
+    order = (0, 1, 2, 1, 0, 2)
+
+    def run():
+        return [avq.avq_cross_attention_backward(*sets[i][0], ws=ws, **sets[i][1]) for i in order]
+
+    def same(got):
+        return all(torch.equal(a, b) for i, g in zip(order, got) for a, b in zip(g, want[i]))
+
+    assert same(run())
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        got = run()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert same(got)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [avq.avq_cross_attention_backward(*sets[i][0], stream=streams[k % 2], **sets[i][1])
+           for k, i in enumerate(order * 4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for k, g in enumerate(got) for a, b in zip(g, want[(order * 4)[k]]))
+    avq.avq_check_device()
